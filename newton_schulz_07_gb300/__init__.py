@@ -1,7 +1,8 @@
 """Batched quintic Newton–Schulz orthogonalisation for GB300 (sm_103a).
 
 The compute path is the CUDA library libmuon_ns.so (C ABI in
-include/muon_ns.h); this package is its thin PyTorch binding.
+include/muon_ns.h, and include/muon_lm.h for the operators at a language
+model's ends); this package is its thin PyTorch binding.
 """
 from ._lib import LIB_PATH, MuonNSError, lib  # noqa: F401
 from .ns import (  # noqa: F401
@@ -39,6 +40,14 @@ from .ns import (  # noqa: F401
     step_workspace_size,
     workspace_region,
     workspace_size,
+)
+from .lm import (  # noqa: F401
+    embed_grad_workspace_size,
+    layer_norm_grad_workspace_size,
+    muon_embed,
+    muon_embed_grad,
+    muon_layer_norm,
+    muon_layer_norm_grad,
 )
 
 __version__ = "0.1.0"

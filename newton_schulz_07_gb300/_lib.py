@@ -1,4 +1,5 @@
-"""ctypes loader for libmuon_ns.so (the C ABI declared in include/muon_ns.h).
+"""ctypes loader for libmuon_ns.so (the C ABI declared in include/muon_ns.h
+and include/muon_lm.h).
 
 The library is built in-tree by newton_schulz_07_gb300.build; there is no
 fallback: if it is missing, every entry point raises.
@@ -98,6 +99,18 @@ SIGNATURES = {
     "muon_ns_tile_coords": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_ll, _pi, _pi, _pi]),
 }
 
+# The operators at a language model's ends (include/muon_lm.h).
+LM_SIGNATURES = {
+    "muon_embed": (_c_int, [_vp, _c_int, _c_ll, _c_int, _vp, _c_int, _c_ll, _c_f, _vp, _c_int, _vp]),
+    "muon_embed_grad_workspace_size": (_c_int, [_c_ll, _c_ll, _c_int, _psz]),
+    "muon_embed_grad": (_c_int, [_vp, _c_int, _vp, _c_int, _c_ll, _c_ll, _c_int, _c_f, _vp, _c_int, _c_int, _vp, _c_sz,
+                                 _vp]),
+    "muon_layer_norm": (_c_int, [_vp, _c_int, _vp, _vp, _c_int, _c_ll, _c_int, _c_f, _vp, _vp, _vp, _vp]),
+    "muon_layer_norm_grad_workspace_size": (_c_int, [_c_ll, _c_int, _psz]),
+    "muon_layer_norm_grad": (_c_int, [_vp, _vp, _c_int, _vp, _c_int, _vp, _vp, _c_ll, _c_int, _vp, _vp, _vp, _vp, _c_sz,
+                                      _vp]),
+}
+
 _lock = threading.Lock()
 _lib = None
 
@@ -121,7 +134,7 @@ def lib() -> ctypes.CDLL:
                     f"{LIB_PATH} is missing: build it with `python -m newton_schulz_07_gb300.build` "
                     "(there is no fallback implementation)")
             L = ctypes.CDLL(LIB_PATH)
-            for name, (res, args) in SIGNATURES.items():
+            for name, (res, args) in {**SIGNATURES, **LM_SIGNATURES}.items():
                 fn = getattr(L, name)
                 fn.restype = res
                 fn.argtypes = args

@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuon_ns.so")
 
-SOURCES = ["muon_ns.cu", "gemm_sym.cu", "gemm_full.cu", "gemm_f32.cu", "gemm_wout.cu", "gemm_wout_grp.cu"]
+SOURCES = ["muon_ns.cu", "gemm_sym.cu", "gemm_full.cu", "gemm_f32.cu", "gemm_wout.cu", "gemm_wout_grp.cu",
+           "lm/embed.cu", "lm/layer_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                      "-I" + INCLUDE, "-I" + CSRC]
@@ -46,13 +47,13 @@ def _stale(target, deps):
 
 def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    headers.append(os.path.join(INCLUDE, "muon_ns.h"))
+    headers = [os.path.join(d, f) for d in (CSRC, os.path.join(CSRC, "lm"), INCLUDE) for f in os.listdir(d)
+               if f.endswith((".h", ".cuh"))]
     jobs = []
     objs = []
     for src in SOURCES:
         srcp = os.path.join(CSRC, src)
-        obj = os.path.join(BUILD, src.replace(".cu", ".o"))
+        obj = os.path.join(BUILD, src.replace("/", "_").replace(".cu", ".o"))
         objs.append(obj)
         if force or _stale(obj, [srcp] + headers):
             jobs.append([nvcc()] + NVCC_FLAGS + list(extra_flags) + ["-c", srcp, "-o", obj])

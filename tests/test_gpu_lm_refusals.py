@@ -1,0 +1,47 @@
+"""What the binding refuses on a GPU: other types, shapes, devices, strided
+tensors and short workspaces, before anything is launched."""
+import pytest
+import torch
+
+import newton_schulz_07_gb300 as ns
+
+pytestmark = pytest.mark.gpu
+
+
+def _c(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype, device="cuda")
+
+
+def test_embedding():
+    table, ids = _c(10, 8), _c(4, dtype=torch.int64)
+    dy = _c(4, 8)
+    for error, f in (
+            (TypeError, lambda: ns.muon_embed(table.half(), ids)), (TypeError, lambda: ns.muon_embed(table, ids.short())),
+            (TypeError, lambda: ns.muon_embed(table, ids.cpu())), (ValueError, lambda: ns.muon_embed(table[0], ids)),
+            (ValueError, lambda: ns.muon_embed(_c(8, 10).t(), ids)), (ValueError, lambda: ns.muon_embed(table, _c(8, dtype=torch.int64)[::2])),
+            (ValueError, lambda: ns.muon_embed(table, ids, out=_c(4, 9))),
+            (ValueError, lambda: ns.muon_embed(table, ids, out=_c(4, 8), dtype=torch.bfloat16)),
+            (ns.MuonNSError, lambda: ns.muon_embed(table, ids, scale=float("nan"))),
+            (ns.MuonNSError, lambda: ns.muon_embed(table, ids, out=table[:4])),
+            (ValueError, lambda: ns.muon_embed_grad(dy, ids[:3], 10)), (ValueError, lambda: ns.muon_embed_grad(dy[0], ids, 10)),
+            (ValueError, lambda: ns.muon_embed_grad(dy, ids, 10, accumulate=True)),
+            (ValueError, lambda: ns.muon_embed_grad(dy, ids, 10, dtable=_c(9, 8))),
+            (ValueError, lambda: ns.muon_embed_grad(dy, ids, 10, workspace=torch.zeros(1 << 16, dtype=torch.uint8))),
+            (ns.MuonNSError, lambda: ns.muon_embed_grad(dy, ids, 10, workspace=_c(8)))):
+        with pytest.raises(error):
+            f()
+
+
+def test_layer_norm():
+    x, w, m = _c(4, 8), _c(8), _c(4)
+    for error, f in (
+            (TypeError, lambda: ns.muon_layer_norm(x.half(), w)), (ValueError, lambda: ns.muon_layer_norm(x, w[:7])),
+            (TypeError, lambda: ns.muon_layer_norm(x, w, w.bfloat16())), (ValueError, lambda: ns.muon_layer_norm(x.t(), _c(4))),
+            (TypeError, lambda: ns.muon_layer_norm(x, w, out=x.bfloat16())), (ns.MuonNSError, lambda: ns.muon_layer_norm(_c(4, 0), _c(0))),
+            (ns.MuonNSError, lambda: ns.muon_layer_norm(x, w, eps=-1.0)), (ValueError, lambda: ns.muon_layer_norm(_c(), w)),
+            (TypeError, lambda: ns.muon_layer_norm_grad(x.bfloat16(), x, w, m, m)),
+            (ValueError, lambda: ns.muon_layer_norm_grad(x[:3], x, w, m, m)), (ValueError, lambda: ns.muon_layer_norm_grad(x, x, w, m[:3], m)),
+            (TypeError, lambda: ns.muon_layer_norm_grad(x, x, w, m.bfloat16(), m)),
+            (ns.MuonNSError, lambda: ns.muon_layer_norm_grad(x, x, w, m, m, workspace=_c(1)))):
+        with pytest.raises(error):
+            f()
