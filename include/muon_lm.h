@@ -83,6 +83,48 @@ int muon_layer_norm_grad(const void* dy, const void* x, int x_type, const void* 
                          const float* mean, const float* rstd, long long rows, int dim, void* dx, float* dweight,
                          float* dbias, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Output head: softmax cross entropy of h W^T over a large vocabulary, without
+ * keeping the logits.  For token n with target t,
+ *   z = h_n W^T,  loss_n = log sum_v exp(z_v) - z_t,
+ * and with g_n = dloss[n] (1 / (tokens with a loss) if dloss is NULL) and
+ * p = softmax(z), the gradient of sum_n g_n loss_n is
+ *   dh_n = g_n (sum_v p_v W_v - W_t),  dW_v = sum_n g_n (p_nv - [v = t_n]) h_n.
+ *   h  bf16 [tokens][dim], W  bf16 [vocab][dim], loss  fp32 [tokens],
+ *   dh  bf16 [tokens][dim], dW  [vocab][dim] of dW_type;
+ *   targets  int32 or int64 [tokens] (target_bits).  A target outside
+ *   [0, vocab) or equal to ignore_index takes the token out: loss 0, dh 0, no
+ *   part in dW, whatever its row of h and its dloss hold, and no work.
+ * dim must be a multiple of 8 (16-byte rows) and h, W, dh and dW 16-byte
+ * aligned: MUON_NS_ERR_ALIGNMENT otherwise.  dh and dW overlap nothing.
+ * Products accumulate in fp32 on the tensor cores; sums, logarithms and the
+ * targets' terms are fp32.  The probabilities enter dh and dW as bf16 operands,
+ * and h with its factor g / s enters dW as bf16.
+ * The device error word is the first int of the workspace, as for muon_ns_ws
+ * (muon_ns_read_error, muon_ns_check; waits bounded by
+ * muon_ns_set_wait_budget); a call on no tokens or no vocabulary leaves it.
+ * ------------------------------------------------------------------------- */
+
+/* Workspace of muon_head_loss (grad = 0) or muon_head_loss_grad (grad != 0).
+ * pieces: pieces of the vocabulary that the gradient is taken in (of whole
+ * 256 columns).  The workspace holds the probabilities of one piece in bf16
+ * (tokens x piece).  With one piece 3 products are computed, with more the
+ * probabilities of all but one piece are computed twice, up to 4.  0: as few
+ * as keep a piece at about 4 GiB.  Ignored for grad = 0. */
+int muon_head_workspace_size(long long tokens, long long vocab, int dim, int grad, int pieces, size_t* bytes);
+
+/* The losses alone. */
+int muon_head_loss(const muon_bf16* h, const muon_bf16* W, long long tokens, long long vocab, int dim,
+                   const void* targets, int target_bits, long long ignore_index, float* loss, void* workspace,
+                   size_t workspace_bytes, cudaStream_t stream);
+
+/* The losses and the gradient in one call.  accumulate != 0 (fp32 dW only):
+ * dW is added to.  dloss: device fp32 [tokens], or NULL. */
+int muon_head_loss_grad(const muon_bf16* h, const muon_bf16* W, long long tokens, long long vocab, int dim,
+                        const void* targets, int target_bits, long long ignore_index, const float* dloss, int pieces,
+                        float* loss, muon_bf16* dh, void* dW, int dW_type, int accumulate, void* workspace,
+                        size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -43,9 +43,12 @@ from .ns import (  # noqa: F401
 )
 from .lm import (  # noqa: F401
     embed_grad_workspace_size,
+    head_workspace_size,
     layer_norm_grad_workspace_size,
     muon_embed,
     muon_embed_grad,
+    muon_head_loss,
+    muon_head_loss_grad,
     muon_layer_norm,
     muon_layer_norm_grad,
 )

@@ -109,6 +109,10 @@ LM_SIGNATURES = {
     "muon_layer_norm_grad_workspace_size": (_c_int, [_c_ll, _c_int, _psz]),
     "muon_layer_norm_grad": (_c_int, [_vp, _vp, _c_int, _vp, _c_int, _vp, _vp, _c_ll, _c_int, _vp, _vp, _vp, _vp, _c_sz,
                                       _vp]),
+    "muon_head_workspace_size": (_c_int, [_c_ll, _c_ll, _c_int, _c_int, _c_int, _psz]),
+    "muon_head_loss": (_c_int, [_vp, _vp, _c_ll, _c_ll, _c_int, _vp, _c_int, _c_ll, _vp, _vp, _c_sz, _vp]),
+    "muon_head_loss_grad": (_c_int, [_vp, _vp, _c_ll, _c_ll, _c_int, _vp, _c_int, _c_ll, _vp, _c_int, _vp, _vp, _vp,
+                                     _c_int, _c_int, _vp, _c_sz, _vp]),
 }
 
 _lock = threading.Lock()

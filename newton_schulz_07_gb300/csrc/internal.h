@@ -70,4 +70,11 @@ cudaError_t launch_sym_mnmn_f32(const GemmParams& p, PairMode mode, int grid, cu
 cudaError_t launch_full_kmn_f32(const GemmParams& p, PairMode mode, int max_k, int grid, cudaStream_t stream);
 cudaError_t launch_full_kk_f32(const GemmParams& p, PairMode mode, int max_k, int grid, cudaStream_t stream);
 
+// Budget of a bounded wait, in clock64 cycles (muon_ns_set_wait_budget).
+long long wait_budget();
+
+// The driver's cuTensorMapEncodeTiled (PFN_cuTensorMapEncodeTiled_v12000), or
+// null if it cannot be had.
+void* tensor_map_encoder();
+
 }  // namespace mns

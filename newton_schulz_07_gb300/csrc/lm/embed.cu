@@ -82,8 +82,9 @@ constexpr size_t kSortSmem = sizeof(int) * kSortWarps * kBins;
 // writes every element to its warp's next position: stable, since a warp
 // takes its elements in order and match_any ranks the lanes of one digit.
 __global__ void __launch_bounds__(32 * kSortWarps)
-    token_sort(const void* __restrict__ ids, int ids64, long long tokens, long long vocab, int passes, int digit_bits,
-               unsigned long long* buf_even, unsigned long long* buf_odd, unsigned int* bitmap, long long words) {
+    token_sort(const void* __restrict__ ids, int ids64, long long tokens, long long vocab, const SortBy by, int passes,
+               int digit_bits, unsigned long long* buf_even, unsigned long long* buf_odd, unsigned int* bitmap,
+               long long words) {
   extern __shared__ int cnt[];  // [kSortWarps][kBins]
   __shared__ int totals[kBins];
   __shared__ int base[kBins];
@@ -101,6 +102,7 @@ __global__ void __launch_bounds__(32 * kSortWarps)
   const long long begin = cta_begin + warp * per_warp;
   long long end = begin + per_warp;
   if (end > cta_end) end = cta_end;
+  const long long none = by.presence ? 1 : vocab;  // key of an id that names no row
   const int bins = 1 << digit_bits;
   int* mine = cnt + warp * kBins;
 
@@ -116,8 +118,10 @@ __global__ void __launch_bounds__(32 * kSortWarps)
     const int shift = 32 + pass * digit_bits;
     auto fetch = [&](long long i) -> unsigned long long {
       if (pass > 0) return __ldcg(src + i);
-      const long long id = load_id(ids, ids64, i, vocab);
-      return (static_cast<unsigned long long>(id < 0 ? vocab : id) << 32) | static_cast<unsigned long long>(i);
+      long long id = load_id(ids, ids64, i, vocab);
+      if (id == by.skip) id = -1;
+      if (by.presence && id >= 0) id = 0;
+      return (static_cast<unsigned long long>(id < 0 ? none : id) << 32) | static_cast<unsigned long long>(i);
     };
     for (int d = lane; d < bins; d += 32) mine[d] = 0;
     __syncwarp();
@@ -204,13 +208,17 @@ __global__ void __launch_bounds__(32 * kSortWarps)
     else
       __syncthreads();
   }
-  if (words > 0) {
-    const unsigned long long* sorted = (passes & 1) ? buf_even : buf_odd;
-    for (long long i = static_cast<long long>(rank) * blockDim.x + tid; i < tokens;
-         i += static_cast<long long>(ctas) * blockDim.x) {
-      const unsigned int k = static_cast<unsigned int>(__ldcg(sorted + i) >> 32);
-      const bool first = i == 0 || static_cast<unsigned int>(__ldcg(sorted + i - 1) >> 32) != k;
-      if (first && k < vocab) atomicOr(bitmap + (k >> 5), 1u << (k & 31));
+  if (words == 0 && by.count == nullptr) return;
+  const unsigned long long* sorted = (passes & 1) ? buf_even : buf_odd;
+  for (long long i = static_cast<long long>(rank) * blockDim.x + tid; i < tokens;
+       i += static_cast<long long>(ctas) * blockDim.x) {
+    const unsigned int k = static_cast<unsigned int>(__ldcg(sorted + i) >> 32);
+    const bool first = i == 0 || static_cast<unsigned int>(__ldcg(sorted + i - 1) >> 32) != k;
+    const bool live = k < none;
+    if (words > 0 && first && live) atomicOr(bitmap + (k >> 5), 1u << (k & 31));
+    if (by.count != nullptr) {
+      if (first && !live) *by.count = static_cast<int>(i);
+      if (live && i == tokens - 1) *by.count = static_cast<int>(tokens);
     }
   }
 }
@@ -228,7 +236,7 @@ struct SumParams {
   const unsigned long long* sorted;
   const unsigned int* bitmap;
   float* partial;  // [pieces][2][dim]: the row that began before the piece, the one that goes on after it
-  const float* coef;  // COMPACT: factor of each token
+  const float* coef;  // COMPACT: factor of each sorted position
   int* slot;          // COMPACT
   long long tokens, vocab, pieces;
   int dim, slices, accumulate;
@@ -323,7 +331,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) row_sums(const SumParams P) {
       const unsigned int ku = __shfl_sync(0xFFFFFFFFu, key, p);
       if (ku == none) continue;
       float f = 1.0f;
-      if (COMPACT) f = P.coef[__shfl_sync(0xFFFFFFFFu, token_of(e), p)];
+      if (COMPACT) f = P.coef[p0 + p];
 #pragma unroll
       for (int k = 0; k < kK; ++k)
         if (slice_col<VEC>(s, lane, k) < P.dim)
@@ -455,9 +463,9 @@ int bits_of(long long v) {
   return b;
 }
 
-// Passes and digit of the sort: keys run from 0 to vocab.
-void sort_plan(long long vocab, int* passes, int* digit) {
-  const int bits = bits_of(vocab);
+// Passes and digit of the sort of keys from 0 to `largest`.
+void sort_plan(long long largest, int* passes, int* digit) {
+  const int bits = bits_of(largest);
   *passes = (bits + kMaxDigit - 1) / kMaxDigit;
   *digit = (bits + *passes - 1) / *passes;
 }
@@ -522,10 +530,10 @@ SumLayout sum_layout(long long tokens, long long vocab, int dim) {
   return L;
 }
 
-cudaError_t launch_sort(const void* ids, int ids64, long long tokens, long long vocab, uint8_t* ws,
+cudaError_t launch_sort(const void* ids, int ids64, long long tokens, long long vocab, const SortBy& by, uint8_t* ws,
                         const SumLayout& L, cudaStream_t stream) {
   int passes, digit;
-  sort_plan(vocab, &passes, &digit);
+  sort_plan(by.presence ? 1 : vocab, &passes, &digit);
   int ctas = 1;
   while (ctas < kSortCluster && static_cast<long long>(ctas) * kSortTokens < tokens) ctas *= 2;
   auto* last = reinterpret_cast<unsigned long long*>(ws + L.sorted);
@@ -540,8 +548,9 @@ cudaError_t launch_sort(const void* ids, int ids64, long long tokens, long long 
     configured.fetch_or(1ull << (dev & 63));
   }
   return mns::launch_pdl_cluster(token_sort, dim3(ctas), dim3(32 * kSortWarps), kSortSmem, stream, ctas, ids, ids64,
-                                 tokens, vocab, passes, digit, (passes & 1) ? last : other, (passes & 1) ? other : last,
-                                 reinterpret_cast<unsigned int*>(ws + L.bitmap), (vocab + 31) / 32);
+                                 tokens, vocab, by, passes, digit, (passes & 1) ? last : other,
+                                 (passes & 1) ? other : last, reinterpret_cast<unsigned int*>(ws + L.bitmap),
+                                 by.presence ? 0 : (vocab + 31) / 32);
 }
 
 cudaError_t launch_row_sums(const void* src, int src_type, long long tokens, long long vocab, int dim, float scale,
@@ -632,7 +641,7 @@ int muon_embed_grad(const void* dy, int dy_type, const void* ids, int ids_bits, 
   if ((s = muon_ns_device_supported(-1)) != MUON_NS_OK) return s;
   if (tokens == 0) return accumulate ? MUON_NS_OK : status_of(cudaMemsetAsync(dtable, 0, table_bytes, stream));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  cudaError_t e = launch_sort(ids, ids_bits == 64 ? 1 : 0, tokens, vocab, ws, L, stream);
+  cudaError_t e = launch_sort(ids, ids_bits == 64 ? 1 : 0, tokens, vocab, SortBy{-1, 0, nullptr}, ws, L, stream);
   if (e != cudaSuccess) return status_of(e);
   return status_of(launch_row_sums(dy, dy_type, tokens, vocab, dim, scale, dtable, dtable_type, accumulate ? 1 : 0, ws,
                                    L, stream));

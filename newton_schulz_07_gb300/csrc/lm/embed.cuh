@@ -19,9 +19,15 @@ struct SumLayout {
 };
 SumLayout sum_layout(long long tokens, long long vocab, int dim);
 
+struct SortBy {
+  long long skip;  // an id to be taken as naming no row (-1: none more)
+  int presence;    // sort by whether an id names a row alone (0: it does, 1: it does not); no bitmap
+  int* count;      // optional, device: how many do
+};
+
 // Sorts the tokens by id (stable): sorted[p] = id << 32 | token, ids outside
 // [0, vocab) last with id = vocab.  Bit v of `bitmap` says whether v occurs.
-cudaError_t launch_sort(const void* ids, int ids64, long long tokens, long long vocab, uint8_t* ws,
+cudaError_t launch_sort(const void* ids, int ids64, long long tokens, long long vocab, const SortBy& by, uint8_t* ws,
                         const SumLayout& L, cudaStream_t stream);
 
 // Row sums by sorted token: out[v] = scale * sum of src[t] over the tokens of
@@ -30,9 +36,9 @@ cudaError_t launch_row_sums(const void* src, int src_type, long long tokens, lon
                             void* out, int out_type, int accumulate, uint8_t* ws, const SumLayout& L,
                             cudaStream_t stream);
 
-// The same into compact rows: sum of coef[t] src[t] over the tokens of v goes
-// to row p of out (fp32 [tokens][dim]), p the sorted position of v's first
-// token; slot[v] = p.  Rows of ids that do not occur have no slot (bitmap).
+// The same into compact rows: sum of coef[p] src[t] over the tokens t of v, p
+// their sorted positions, goes to row q of out (fp32 [tokens][dim]), q the position of the first of
+// them; slot[v] = q.  Rows of ids that do not occur have no slot (bitmap).
 cudaError_t launch_row_sums_compact(const void* src, const float* coef, long long tokens, long long vocab, int dim,
                                     float* out, int* slot, uint8_t* ws, const SumLayout& L, cudaStream_t stream);
 

@@ -1,0 +1,602 @@
+// The output head's cross entropy and its gradient, without keeping the
+// logits.
+//
+//   z = h W^T, loss_n = log sum_v exp z_nv - z_nt, p = softmax(z),
+//   dz_nv = g_n (p_nv - [v = t_n]), dh = dz W, dW = dz^T h.
+//
+// Every row is referred to its target's own logit c_n = z_nt, one dot product
+// known before the large one: with e_nv = exp(z_nv - c_n) and s_n = sum_v e_nv,
+//   loss_n = log s_n,  dz_nv = (g_n / s_n) e_nv for v != t,
+//   dz_nt = -g_n (s_n - e_nt) / s_n.
+// So the large product's epilogue takes exponentials and their sum in one
+// pass with no running maximum, and e needs no second pass once s is known:
+// g_n / s_n is a factor of row n of dh, and of row n of h in dW.  The target's
+// own term, which cancels and would lose its digits in bf16, is set to zero in
+// e and added to dh and dW in fp32.  s_n >= e_nt = 1 by construction, so only a
+// logit far above the target's (a loss above log kTopSum = 44) can leave the
+// range: such rows take their largest logit as reference and the tiles that
+// hold them are computed again; the launches that do so leave at once when
+// there are none.
+//
+// Tokens without a loss (target out of range or ignored) are sorted to the
+// end and take no part in the products.  The rest is sorted by target, so the
+// targets' terms of dW are row sums by sorted token, as in the embedding's
+// gradient.
+//
+// The vocabulary is taken in pieces.  With one piece e (bf16, tokens x piece)
+// is held from the first product: 3 products in all.  With more, a first pass
+// over the pieces takes only the sums and keeps the last piece's e; the others
+// are computed again when their turn comes, into the same buffer.
+//
+// Bound by the tensor cores for more than about 200 tokens; below that by
+// reading W twice and writing dW.
+#include <atomic>
+#include <cmath>
+
+#include <cudaTypedefs.h>
+
+#include "lm/common.cuh"
+#include "lm/embed.cuh"
+#include "lm/head_gemm.cuh"
+
+namespace mns {
+namespace lm {
+
+namespace {
+
+constexpr float kTopSum = 1.8446744e19f;  // 2^64
+constexpr int kHeadPairs = 76;            // CTA pairs the splits are chosen for
+constexpr int kHeadGroup = 8;             // pair rows walked together
+constexpr long long kPieceBytes = 1LL << 32;  // e of one piece, at most, by default
+
+// Splits of the vocabulary in dh, by the 256 threads of a CTA: output tiles
+// alone may be too few for the pairs, or fill their last turn badly.  A turn
+// costs its k-blocks and an epilogue worth about 6 of them; the fewest splits
+// of least cost are taken, at most 4 tiles a pair in all and 8 k-blocks each at
+// least.
+__device__ int choose_splits(int tiles, int kb) {
+  __shared__ unsigned long long best;
+  if (threadIdx.x == 0) best = ~0ull;
+  __syncthreads();
+  for (int s = threadIdx.x + 1; s <= 4 * kHeadPairs; s += 256) {
+    if (s > 1 && (static_cast<long long>(s) * tiles > 4 * kHeadPairs || kb / s < 8)) break;
+    const long long turns = (static_cast<long long>(tiles) * s + kHeadPairs - 1) / kHeadPairs;
+    const unsigned long long cost = static_cast<unsigned long long>(turns * ((kb + s - 1) / s + 6));
+    atomicMin(&best, (cost << 16) | static_cast<unsigned long long>(s));
+  }
+  __syncthreads();
+  return static_cast<int>(best & 0xFFFFu);
+}
+
+struct HeadRows {
+  const unsigned long long* sorted;  // key << 32 | token, live tokens first
+  const void* targets;
+  int ids64;
+  long long tokens, vocab;
+  int dim;
+  int* ctl;
+  int* redo;   // per pair row
+  float* zt;   // target's logit
+  float* ref;  // reference of the exponentials
+  float* scale;  // g / s
+  float* coef;   // -g (s - e_t) / s
+};
+
+// Compact copy of the live tokens' h, and the target's logit of each: a warp a
+// row.  The first CTA clears the control words and chooses dh's splits.
+__global__ void __launch_bounds__(256)
+    head_prepare(const HeadRows R, const bf16* __restrict__ h, const bf16* __restrict__ W, bf16* __restrict__ hc,
+                 int pair_rows, int split_kb) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int count = R.ctl[kCtlCount];
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < pair_rows; i += 256) R.redo[i] = 0;
+    const long long tiles = static_cast<long long>(token_pairs(count)) * ((R.dim + kHeadRows - 1) / kHeadRows);
+    const int splits = tiles > 4 * kHeadPairs ? 1 : choose_splits(static_cast<int>(tiles), split_kb);
+    if (threadIdx.x == 0) {
+      R.ctl[kCtlErr] = 0;
+      R.ctl[kCtlRedo] = 0;
+      R.ctl[kCtlSplits] = splits;
+    }
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long p = static_cast<long long>(blockIdx.x) * 8 + warp;
+  if (p >= count) return;
+  const unsigned int token = static_cast<unsigned int>(R.sorted[p]);
+  const long long t = load_id(R.targets, R.ids64, token, R.vocab);
+  const bf16* hr = h + static_cast<long long>(token) * R.dim;
+  const bf16* wr = W + t * R.dim;
+  bf16* out = hc + p * R.dim;
+  float a[8] = {};
+#pragma unroll 4
+  for (int c = lane * 8; c < R.dim; c += 256) {
+    const Vec<bf16, 8> x = load_vec<bf16, 8>(hr + c), w = load_vec<bf16, 8>(wr + c);
+    *reinterpret_cast<Vec<bf16, 8>*>(out + c) = x;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = fmaf(to_f32(x.v[j]), to_f32(w.v[j]), a[j]);
+  }
+  const float z = warp_sum(((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7])));
+  if (lane == 0) {
+    R.zt[p] = z;
+    R.ref[p] = z;
+  }
+}
+
+struct HeadFinish {
+  const float2* stat;
+  int halves;  // statistics a row
+  int again;   // second pass: the rows of tiles that were computed again
+  const float* dloss;  // per token, or null: 1 / count
+  float* loss;         // per token
+  // gradient
+  const bf16* hc;
+  bf16* hs;   // (g / s) h, rows up to a multiple of 64 zero
+  bf16* e;    // the piece held, its first column v0 and its columns
+  long long lde, v0;
+  int vp;
+};
+
+// A CTA a sorted position: joins the row's sums in a fixed order, and from
+// them the loss, the factors of the gradient and the scaled row of h.
+__global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadFinish F) {
+  __shared__ float red[2][4];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  if (F.again && R.ctl[kCtlRedo] == 0) return;
+  const int count = R.ctl[kCtlCount];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (long long p = blockIdx.x; p < R.tokens; p += gridDim.x) {
+    const unsigned int token = static_cast<unsigned int>(R.sorted[p]);
+    if (p >= count) {
+      if (F.again) continue;
+      if (tid == 0) F.loss[token] = 0.0f;
+      // dW's last k-block reads rows up to a multiple of 64.
+      if (F.hs != nullptr && p < (count > 0 ? (count + 63) / 64 * 64 : 64))
+        for (int c = tid * 8; c < R.dim; c += 1024)
+          *reinterpret_cast<uint4*>(F.hs + p * R.dim + c) = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
+    if (F.again && R.redo[p / kHeadRows] == 0) continue;
+    const float2* st = F.stat + p * F.halves;
+    float mx = -INFINITY, s = 0.0f;
+    for (int i = tid; i < F.halves; i += 128) {
+      const float2 v = st[i];
+      mx = fmaxf(mx, v.x);
+      s += v.y;
+    }
+    s = warp_sum(s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    __syncthreads();  // the last row's sums have been read
+    if (lane == 0) {
+      red[0][warp] = s;
+      red[1][warp] = mx;
+    }
+    __syncthreads();
+    s = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
+    mx = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
+    if (!F.again && !(s <= kTopSum)) {  // out of range, or not a number
+      if (tid == 0) {
+        R.ref[p] = mx;
+        R.redo[p / kHeadRows] = 1;
+        R.ctl[kCtlRedo] = 1;
+      }
+      continue;
+    }
+    const float zt = R.zt[p], c = R.ref[p];
+    if (tid == 0) F.loss[token] = logf(s) + (c - zt);
+    if (F.hs == nullptr) continue;
+    const float g = F.dloss != nullptr ? F.dloss[token] : 1.0f / static_cast<float>(count);
+    const float f = g / s;
+    const long long t = load_id(R.targets, R.ids64, token, R.vocab);
+    if (tid == 0) {
+      R.scale[p] = f;
+      R.coef[p] = -g * ((s - expf(zt - c)) / s);
+      if (t >= F.v0 && t < F.v0 + F.vp) F.e[p * F.lde + (t - F.v0)] = 0;
+    }
+    // hs is the MMAs' bf16 operand: one more rounding, up to 2^-8, in each term of
+    // dW but the targets', which are added in fp32.
+    for (int col = tid * 8; col < R.dim; col += 1024) {
+      const Vec<bf16, 8> x = load_vec<bf16, 8>(F.hc + p * R.dim + col);
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = f * to_f32(x.v[j]);
+      store_vec<bf16, 8>(F.hs + p * R.dim + col, o);
+    }
+  }
+}
+
+// The targets' terms of a piece that was computed again.
+__global__ void __launch_bounds__(256)
+    head_clear_targets(const HeadRows R, bf16* __restrict__ e, long long lde, long long v0, int vp) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const long long p = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (p >= R.ctl[kCtlCount]) return;
+  const long long t = load_id(R.targets, R.ids64, static_cast<unsigned int>(R.sorted[p]), R.vocab);
+  if (t >= v0 && t < v0 + vp) e[p * lde + (t - v0)] = 0;
+}
+
+// dh[token] = scale (sum of the splits) + coef W[target], 8 columns a thread.
+__global__ void __launch_bounds__(256)
+    head_join_dh(const HeadRows R, const float* __restrict__ part, const bf16* __restrict__ W, bf16* __restrict__ dh) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int count = R.ctl[kCtlCount], splits = R.ctl[kCtlSplits];
+  const long long rows = static_cast<long long>(token_pairs(count)) * kHeadRows;
+  const int per = R.dim / 8;
+  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const long long p = i / per;
+  if (p >= R.tokens) return;
+  const int c = static_cast<int>(i - p * per) * 8;
+  const unsigned int token = static_cast<unsigned int>(R.sorted[p]);
+  float o[8] = {};
+  if (p < count) {
+    const long long t = load_id(R.targets, R.ids64, token, R.vocab);
+    const Vec<bf16, 8> w = load_vec<bf16, 8>(W + t * R.dim + c);
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const Vec<float, 8> v = load_vec<float, 8>(part + (s * rows + p) * R.dim + c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] += v.v[j];
+    }
+    const float f = R.scale[p], k = R.coef[p];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = fmaf(f, o[j], k * to_f32(w.v[j]));
+  }
+  store_vec<bf16, 8>(dh + static_cast<long long>(token) * R.dim + c, o);
+}
+
+// -------------------------------------------------------------------- host --
+
+struct HeadLayout {
+  size_t redo, zt, ref, scale, coef, stat, sums, slot, hc, hs, addend, e, part, total;
+  SumLayout sum;
+  long long piece, pieces, lde, part_rows;
+  int halves;
+};
+
+int check(long long tokens, long long vocab, int dim, int bits) {
+  if (tokens < 0 || vocab < 0 || dim <= 0 || tokens > kMaxRows || vocab > kMaxRows || dim > kMaxDim)
+    return MUON_NS_ERR_INVALID_ARG;
+  if (bits != 32 && bits != 64) return MUON_NS_ERR_INVALID_ARG;
+  if (dim % 8 != 0) return MUON_NS_ERR_ALIGNMENT;
+  return MUON_NS_OK;
+}
+
+HeadLayout head_layout(long long tokens, long long vocab, int dim, bool grad, int pieces) {
+  HeadLayout L = {};
+  const long long pair_rows = (tokens + kHeadRows - 1) / kHeadRows;
+  // Pieces of whole column tiles.
+  long long n = grad ? pieces : 1;
+  if (n <= 0) n = (2 * tokens * vocab + kPieceBytes - 1) / kPieceBytes;
+  const long long tiles = (vocab + kHeadRows - 1) / kHeadRows;
+  if (n > tiles) n = tiles;
+  if (n < 1) n = 1;
+  L.piece = (tiles + n - 1) / n * kHeadRows;
+  L.pieces = (vocab + L.piece - 1) / L.piece;
+  L.lde = L.piece;
+  L.halves = static_cast<int>((vocab + kHeadHalf - 1) / kHeadHalf);
+  size_t off = sizeof(int) * kCtlWords;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  const size_t n_tok = static_cast<size_t>(tokens);
+  L.redo = take(4 * static_cast<size_t>(pair_rows));
+  L.zt = take(4 * n_tok);
+  L.ref = take(4 * n_tok);
+  L.scale = take(4 * n_tok);
+  L.coef = take(4 * n_tok);
+  L.stat = take(8 * n_tok * L.halves);
+  L.sum = grad ? sum_layout(tokens, vocab, dim) : sum_layout(tokens, 0, 0);
+  L.sums = take(L.sum.total);
+  L.hc = take(2 * n_tok * dim);
+  if (grad) {
+    L.slot = take(4 * static_cast<size_t>(vocab));
+    L.hs = take(2 * n_tok * dim);
+    L.addend = take(4 * n_tok * dim);
+    L.e = take(2 * n_tok * static_cast<size_t>(L.lde));
+    // Rows of the splits: choose_splits takes one, or as many as make at most
+    // 4 kHeadPairs tiles.
+    const long long tn = (dim + kHeadRows - 1) / kHeadRows;
+    long long rows = 4 * kHeadPairs / tn;
+    if (rows < pair_rows) rows = pair_rows;
+    L.part_rows = rows * kHeadRows;
+    L.part = take(4 * static_cast<size_t>(L.part_rows) * dim);
+  }
+  L.total = off;
+  return L;
+}
+
+// Map over rows x inner elements with a row stride of ld elements.
+bool map2d(CUtensorMap* map, const void* base, long long inner, long long rows, long long ld, int box_inner,
+           int box_rows, bool f32 = false) {
+  auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(mns::tensor_map_encoder());
+  if (!fn) return false;
+  const cuuint64_t eb = f32 ? 4 : 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows), 1};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * eb, static_cast<cuuint64_t>(ld) * eb * rows};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+            dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE>
+cudaError_t launch_gemm(const HeadGemm& P, long long units, cudaStream_t stream) {
+  static std::atomic<int> resident[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int most = resident[dev & 63].load();
+  if (most == 0) {
+    e = cudaFuncSetAttribute(head_gemm<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeadSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kHeadThreads);
+    cfg.dynamicSmemBytes = kHeadSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&most, head_gemm<MODE>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (most < 1) return cudaErrorInvalidConfiguration;
+    resident[dev & 63].store(most);
+  }
+  const unsigned n = static_cast<unsigned>(units < most ? units : most);
+  return mns::launch_pdl_cluster(head_gemm<MODE>, dim3(2 * n), dim3(kHeadThreads), kHeadSmem, stream, 2, P);
+}
+
+struct HeadCall {
+  const bf16 *h, *W;
+  long long tokens, vocab;
+  int dim;
+  const void* targets;
+  int ids64;
+  long long skip;
+  const float* dloss;
+  float* loss;
+  bf16* dh;
+  void* dW;
+  int dW_f32, accumulate;
+  uint8_t* ws;
+  cudaStream_t stream;
+};
+
+#define MNS_TRY(x)                                    \
+  do {                                                \
+    const cudaError_t mns_e = (x);                    \
+    if (mns_e != cudaSuccess) return status_of(mns_e); \
+  } while (0)
+
+int run_head(const HeadCall& C, const HeadLayout& L) {
+  const bool grad = C.dh != nullptr;
+  uint8_t* ws = C.ws;
+  const long long N = C.tokens, V = C.vocab;
+  const int D = C.dim;
+  const long long pair_rows = (N + kHeadRows - 1) / kHeadRows, dim_tiles = (D + kHeadRows - 1) / kHeadRows;
+  auto at = [&](size_t off) { return ws + off; };
+  auto f32_at = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+  HeadRows R = {};
+  R.sorted = reinterpret_cast<const unsigned long long*>(at(L.sums + L.sum.sorted));
+  R.targets = C.targets;
+  R.ids64 = C.ids64;
+  R.tokens = N;
+  R.vocab = V;
+  R.dim = D;
+  R.ctl = reinterpret_cast<int*>(ws);
+  R.redo = reinterpret_cast<int*>(at(L.redo));
+  R.zt = f32_at(L.zt);
+  R.ref = f32_at(L.ref);
+  R.scale = f32_at(L.scale);
+  R.coef = f32_at(L.coef);
+  bf16* hc = reinterpret_cast<bf16*>(at(L.hc));
+  bf16* hs = reinterpret_cast<bf16*>(at(L.hs));
+  bf16* e = reinterpret_cast<bf16*>(at(L.e));
+
+  MNS_TRY(launch_sort(C.targets, C.ids64, N, V, SortBy{C.skip, grad ? 0 : 1, R.ctl + kCtlCount}, at(L.sums), L.sum,
+                      C.stream));
+  auto width = [&](long long j) { return V - j * L.piece < L.piece ? V - j * L.piece : L.piece; };
+  // Splits are the same for every piece: chosen for the shortest.
+  const int split_kb = static_cast<int>((width(L.pieces - 1) + kBlockK - 1) / kBlockK);
+  MNS_TRY(mns::launch_pdl(head_prepare, dim3(static_cast<unsigned>((N + 7) / 8)), dim3(256), 0, C.stream, R, C.h, C.W,
+                          hc, static_cast<int>(pair_rows), split_kb));
+
+  HeadGemm G = {};
+  G.ctl = R.ctl;
+  G.dim = D;
+  G.group = kHeadGroup;
+  G.budget = mns::wait_budget();
+  auto logits = [&](long long j, bool stats, bool store, const int* redo) -> int {
+    HeadGemm P = G;
+    P.vp = static_cast<int>(width(j));
+    P.ref = R.ref;
+    P.stat = stats ? reinterpret_cast<float2*>(at(L.stat)) : nullptr;
+    P.stat_ld = L.halves;
+    P.stat0 = static_cast<int>(j * L.piece / kHeadHalf);
+    P.store = store ? 1 : 0;
+    P.redo = redo;
+    if (!map2d(&P.tmA, hc, D, N, D, kBlockK, kTileM) ||
+        !map2d(&P.tmB, C.W + j * L.piece * D, D, P.vp, D, kBlockK, kTileN / 2) ||
+        (store && !map2d(&P.tmOut, e, P.vp, N, L.lde, 64, 32)))
+      return MUON_NS_ERR_CUDA;
+    return status_of(launch_gemm<kLogits>(P, pair_rows * ((P.vp + kHeadRows - 1) / kHeadRows), C.stream));
+  };
+  const long long kept = L.pieces - 1;  // piece whose e the first pass leaves
+  HeadFinish F = {};
+  F.stat = reinterpret_cast<const float2*>(at(L.stat));
+  F.halves = L.halves;
+  F.dloss = C.dloss;
+  F.loss = C.loss;
+  if (grad) {
+    F.hc = hc;
+    F.hs = hs;
+    F.e = e;
+    F.lde = L.lde;
+    F.v0 = kept * L.piece;
+    F.vp = static_cast<int>(width(kept));
+  }
+  const unsigned finish_grid = static_cast<unsigned>(N < 152 * 16 ? N : 152 * 16);
+  for (int again = 0; again < 2; ++again) {
+    for (long long j = 0; j < L.pieces; ++j) {
+      const int s = logits(j, true, grad && j == kept, again ? R.redo : nullptr);
+      if (s != MUON_NS_OK) return s;
+    }
+    F.again = again;
+    MNS_TRY(mns::launch_pdl(head_finish, dim3(finish_grid), dim3(128), 0, C.stream, R, F));
+  }
+  if (!grad) return MUON_NS_OK;
+
+  float* addend = f32_at(L.addend);
+  int* slot = reinterpret_cast<int*>(at(L.slot));
+  MNS_TRY(launch_row_sums_compact(C.h, R.coef, N, V, D, addend, slot, at(L.sums), L.sum, C.stream));
+  for (long long i = 0; i < L.pieces; ++i) {
+    const long long j = i == 0 ? kept : i - 1;
+    const long long v0 = j * L.piece;
+    const int vp = static_cast<int>(width(j));
+    if (i > 0) {
+      const int s = logits(j, false, true, nullptr);
+      if (s != MUON_NS_OK) return s;
+      MNS_TRY(mns::launch_pdl(head_clear_targets, dim3(static_cast<unsigned>((N + 255) / 256)), dim3(256), 0, C.stream,
+                              R, e, L.lde, v0, vp));
+    }
+    HeadGemm P = G;
+    P.vp = vp;
+    P.add = i > 0 ? 1 : 0;
+    if (!map2d(&P.tmA, e, vp, N, L.lde, kBlockK, kTileM) || !map2d(&P.tmB, C.W + v0 * D, D, vp, D, 64, kBlockK) ||
+        !map2d(&P.tmOut, at(L.part), D, L.part_rows, D, 32, 32, true))
+      return MUON_NS_ERR_CUDA;
+    // At most one tile a split more than choose_splits may take.
+    const long long most = pair_rows * dim_tiles > 4 * kHeadPairs ? pair_rows * dim_tiles : 4 * kHeadPairs;
+    MNS_TRY(launch_gemm<kDh>(P, most, C.stream));
+    P = G;
+    P.vp = vp;
+    P.add = C.accumulate;
+    P.addend = addend;
+    P.slot = slot;
+    P.bitmap = reinterpret_cast<const unsigned int*>(at(L.sums + L.sum.bitmap));
+    P.v0 = v0;
+    void* dst = static_cast<uint8_t*>(C.dW) + static_cast<size_t>(v0) * D * (C.dW_f32 ? 4 : 2);
+    if (!map2d(&P.tmA, e, vp, N, L.lde, 64, kBlockK) || !map2d(&P.tmB, hs, D, N, D, 64, kBlockK) ||
+        !map2d(&P.tmOut, dst, D, vp, D, C.dW_f32 ? 32 : 64, 32, C.dW_f32 != 0))
+      return MUON_NS_ERR_CUDA;
+    const long long units = static_cast<long long>((vp + kHeadRows - 1) / kHeadRows) * dim_tiles;
+    MNS_TRY(C.dW_f32 ? launch_gemm<kDwF32>(P, units, C.stream) : launch_gemm<kDwBf16>(P, units, C.stream));
+  }
+  const long long vecs = N * (D / 8);
+  MNS_TRY(mns::launch_pdl(head_join_dh, dim3(static_cast<unsigned>((vecs + 255) / 256)), dim3(256), 0, C.stream, R,
+                          static_cast<const float*>(f32_at(L.part)), C.W, C.dh));
+  return MUON_NS_OK;
+}
+
+}  // namespace
+
+}  // namespace lm
+}  // namespace mns
+
+using namespace mns::lm;
+
+namespace {
+
+inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+int muon_head_workspace_size(long long tokens, long long vocab, int dim, int grad, int pieces, size_t* bytes) {
+  const int s = check(tokens, vocab, dim, 32);
+  if (s != MUON_NS_OK) return s;
+  if (!bytes || pieces < 0) return MUON_NS_ERR_INVALID_ARG;
+  *bytes = tokens == 0 || vocab == 0 ? 0 : head_layout(tokens, vocab, dim, grad != 0, pieces).total;
+  return MUON_NS_OK;
+}
+
+int muon_head_loss(const muon_bf16* h, const muon_bf16* W, long long tokens, long long vocab, int dim,
+                   const void* targets, int target_bits, long long ignore_index, float* loss, void* workspace,
+                   size_t workspace_bytes, cudaStream_t stream) {
+  int s = check(tokens, vocab, dim, target_bits);
+  if (s != MUON_NS_OK) return s;
+  if (tokens == 0) return MUON_NS_OK;
+  if (!h || !targets || !loss || (vocab > 0 && !W)) return MUON_NS_ERR_INVALID_ARG;
+  if (!aligned(h, 16) || !aligned(W, 16) || !aligned(loss, 4) || !aligned(targets, target_bits / 8))
+    return MUON_NS_ERR_ALIGNMENT;
+  const HeadLayout L = head_layout(tokens, vocab, dim, false, 1);
+  if (vocab > 0 && (!workspace || workspace_bytes < L.total)) return MUON_NS_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MUON_NS_ERR_ALIGNMENT;
+  if ((s = muon_ns_device_supported(-1)) != MUON_NS_OK) return s;
+  if (vocab == 0) return status_of(cudaMemsetAsync(loss, 0, sizeof(float) * tokens, stream));
+  HeadCall C = {};
+  C.h = h;
+  C.W = W;
+  C.tokens = tokens;
+  C.vocab = vocab;
+  C.dim = dim;
+  C.targets = targets;
+  C.ids64 = target_bits == 64 ? 1 : 0;
+  C.skip = ignore_index;
+  C.loss = loss;
+  C.ws = static_cast<uint8_t*>(workspace);
+  C.stream = stream;
+  return run_head(C, L);
+}
+
+int muon_head_loss_grad(const muon_bf16* h, const muon_bf16* W, long long tokens, long long vocab, int dim,
+                        const void* targets, int target_bits, long long ignore_index, const float* dloss, int pieces,
+                        float* loss, muon_bf16* dh, void* dW, int dW_type, int accumulate, void* workspace,
+                        size_t workspace_bytes, cudaStream_t stream) {
+  int s = check(tokens, vocab, dim, target_bits);
+  if (s != MUON_NS_OK) return s;
+  if (pieces < 0 || !type_ok(dW_type)) return MUON_NS_ERR_INVALID_ARG;
+  if (accumulate && dW_type != MUON_LM_F32) return MUON_NS_ERR_INVALID_ARG;
+  if (tokens > 0 && (!h || !targets || !loss || !dh)) return MUON_NS_ERR_INVALID_ARG;
+  if (vocab > 0 && (!dW || (tokens > 0 && !W))) return MUON_NS_ERR_INVALID_ARG;
+  if (!aligned(h, 16) || !aligned(W, 16) || !aligned(dh, 16) || !aligned(dW, 16) || !aligned(loss, 4) ||
+      !aligned(dloss, 4) || !aligned(targets, target_bits / 8))
+    return MUON_NS_ERR_ALIGNMENT;
+  const size_t hb = 2 * static_cast<size_t>(tokens) * dim, wb = 2 * static_cast<size_t>(vocab) * dim;
+  const size_t db = static_cast<size_t>(vocab) * dim * type_size(dW_type);
+  if (overlap(dh, hb, h, hb) || overlap(dh, hb, W, wb) || overlap(dW, db, h, hb) || overlap(dW, db, W, wb) ||
+      overlap(dh, hb, dW, db))
+    return MUON_NS_ERR_INVALID_ARG;
+  const HeadLayout L = head_layout(tokens, vocab, dim, true, pieces);
+  if (tokens > 0 && vocab > 0 && (!workspace || workspace_bytes < L.total)) return MUON_NS_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MUON_NS_ERR_ALIGNMENT;
+  if ((s = muon_ns_device_supported(-1)) != MUON_NS_OK) return s;
+  if (tokens == 0 || vocab == 0) {
+    cudaError_t e = cudaSuccess;
+    if (tokens > 0) e = cudaMemsetAsync(loss, 0, sizeof(float) * tokens, stream);
+    if (e == cudaSuccess && tokens > 0) e = cudaMemsetAsync(dh, 0, hb, stream);
+    if (e == cudaSuccess && vocab > 0 && !accumulate) e = cudaMemsetAsync(dW, 0, db, stream);
+    return status_of(e);
+  }
+  HeadCall C = {};
+  C.h = h;
+  C.W = W;
+  C.tokens = tokens;
+  C.vocab = vocab;
+  C.dim = dim;
+  C.targets = targets;
+  C.ids64 = target_bits == 64 ? 1 : 0;
+  C.skip = ignore_index;
+  C.dloss = dloss;
+  C.loss = loss;
+  C.dh = dh;
+  C.dW = dW;
+  C.dW_f32 = dW_type == MUON_LM_F32 ? 1 : 0;
+  C.accumulate = accumulate ? 1 : 0;
+  C.ws = static_cast<uint8_t*>(workspace);
+  C.stream = stream;
+  return run_head(C, L);
+}
+
+}  // extern "C"

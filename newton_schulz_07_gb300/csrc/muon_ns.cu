@@ -286,8 +286,7 @@ mns::GemmParams* new_params(int ng, float alpha, float beta, float eps, int* err
   P.beta = beta;
   P.eps = eps;
   P.err = err;
-  const long long budget = g_wait_budget.load();
-  P.budget = budget > 0 ? budget : kWaitBudgetCycles;
+  P.budget = mns::wait_budget();
   return &P;
 }
 
@@ -750,6 +749,17 @@ std::mutex g_cache_mu;
 Cache g_cache[64];
 
 }  // namespace
+
+namespace mns {
+
+long long wait_budget() {
+  const long long budget = g_wait_budget.load();
+  return budget > 0 ? budget : kWaitBudgetCycles;
+}
+
+void* tensor_map_encoder() { return reinterpret_cast<void*>(encode_fn()); }
+
+}  // namespace mns
 
 extern "C" {
 

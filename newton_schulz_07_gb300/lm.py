@@ -188,3 +188,70 @@ def muon_layer_norm_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor
           rstd.data_ptr(), rows, dim, dx.data_ptr(), grads.data_ptr(), dbias.data_ptr() if bias else None,
           workspace.data_ptr(), _nbytes(workspace))
     return dx, grads[0], dbias
+
+
+# -------------------------------------------------------------------- head --
+
+_BF16 = {torch.bfloat16: 0}
+
+
+def head_workspace_size(tokens: int, vocab: int, dim: int, grad: bool = True, pieces: int = 0) -> int:
+    return _size("muon_head_workspace_size", int(tokens), int(vocab), int(dim), int(bool(grad)), int(pieces))
+
+
+def _head_args(h, table, targets):
+    _tensor(h, "h", _BF16)
+    dev = h.device
+    _tensor(table, "table", _BF16, dev)
+    bits = _tensor(targets, "targets", _IDS, dev)
+    if h.dim() < 1 or table.dim() != 2 or table.shape[1] != h.shape[-1]:
+        raise ValueError(f"h and table must be [...][dim] and [vocab][dim], got {tuple(h.shape)} and {tuple(table.shape)}")
+    _shaped(targets, h.shape[:-1], "targets")
+    return dev, bits, targets.numel(), table.shape[0], table.shape[1]
+
+
+def muon_head_loss(h: torch.Tensor, table: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
+                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Cross entropy of softmax(h table^T) at `targets`, a loss a token (fp32
+    of targets' shape), without keeping the logits.  h and table are bfloat16;
+    targets int32 or int64.  Tokens whose target is ignore_index or outside
+    the table have loss 0."""
+    dev, bits, n, vocab, dim = _head_args(h, table, targets)
+    loss = torch.empty(targets.shape, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = _workspace(None, head_workspace_size(n, vocab, dim, False), dev)
+    else:
+        _workspace(workspace, 0, dev)
+    _call("muon_head_loss", dev, h.data_ptr(), table.data_ptr(), n, vocab, dim, targets.data_ptr(), bits,
+          int(ignore_index), loss.data_ptr(), workspace.data_ptr(), _nbytes(workspace))
+    return loss
+
+
+def muon_head_loss_grad(h: torch.Tensor, table: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
+                        dloss: torch.Tensor | None = None, dtable: torch.Tensor | None = None,
+                        accumulate: bool = False, pieces: int = 0, workspace: torch.Tensor | None = None):
+    """(loss, dh, dtable): muon_head_loss and the gradient of sum(dloss * loss)
+    in one call; dloss (fp32 of targets' shape) defaults to the mean's, 1 / the
+    number of tokens with a loss.  dh is bfloat16; dtable bfloat16 unless a
+    float32 `dtable` is given, to which `accumulate` adds.  `pieces` of the
+    vocabulary bound the workspace (0: pieces of about 4 GiB)."""
+    dev, bits, n, vocab, dim = _head_args(h, table, targets)
+    if dloss is not None:
+        _tensor(dloss, "dloss", _F32, dev)
+        _shaped(dloss, targets.shape, "dloss")
+    if dtable is None:
+        if accumulate:
+            raise ValueError("accumulate needs the dtable to add to")
+        dtable = torch.empty_like(table)
+    dt = _tensor(dtable, "dtable", device=dev)
+    _shaped(dtable, table.shape, "dtable")
+    loss = torch.empty(targets.shape, dtype=torch.float32, device=dev)
+    dh = torch.empty_like(h)
+    if workspace is None:
+        workspace = _workspace(None, head_workspace_size(n, vocab, dim, True, pieces), dev)
+    else:
+        _workspace(workspace, 0, dev)
+    _call("muon_head_loss_grad", dev, h.data_ptr(), table.data_ptr(), n, vocab, dim, targets.data_ptr(), bits,
+          int(ignore_index), None if dloss is None else dloss.data_ptr(), int(pieces), loss.data_ptr(), dh.data_ptr(),
+          dtable.data_ptr(), dt, int(bool(accumulate)), workspace.data_ptr(), _nbytes(workspace))
+    return loss, dh, dtable
