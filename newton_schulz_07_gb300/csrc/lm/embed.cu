@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(256)
     Vec<TI, VEC> v[kLookups];
 #pragma unroll
     for (int u = 0; u < kLookups; ++u)
-      if (id[u] >= 0) v[u] = load_vec<TI, VEC>(table + id[u] * dim + c);
+      if (id[u] >= 0) v[u] = load_global<TI, VEC>(table + id[u] * dim + c);
 #pragma unroll
     for (int u = 0; u < kLookups; ++u) {
       const long long t = t0 + u * rows;
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(256)
         float o[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) o[j] = id[u] >= 0 ? scale * to_f32(v[u].v[j]) : 0.0f;
-        store_vec<TO, VEC>(out + t * dim + c, o);
+        store_global<TO, VEC>(out + t * dim + c, o);
       }
     }
   }
@@ -263,11 +263,11 @@ __device__ __forceinline__ void write_row(TO* row, int s, int lane, int dim, flo
 #pragma unroll
       for (int j = 0; j < VEC; ++j) o[j] = scale * a[k][j];
       if (accumulate) {
-        const Vec<TO, VEC> old = load_vec<TO, VEC>(row + c);
+        const Vec<TO, VEC> old = load_global<TO, VEC>(row + c);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) o[j] += to_f32(old.v[j]);
       }
-      store_vec<TO, VEC>(row + c, o);
+      store_global<TO, VEC>(row + c, o);
     }
   }
 }
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) row_sums(const SumParams P) {
     const float zero[VEC] = {};
     for (int r = 0; r < kZeroRows; ++r)
       if (v0 + r < P.vocab && !((bits >> r) & 1u))
-        for (int c = lane * VEC; c < P.dim; c += 32 * VEC) store_vec<TO, VEC>(out + (v0 + r) * P.dim + c, zero);
+        for (int c = lane * VEC; c < P.dim; c += 32 * VEC) store_global<TO, VEC>(out + (v0 + r) * P.dim + c, zero);
     return;
   }
   const long long piece = item / P.slices;
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) row_sums(const SumParams P) {
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
           const int c = slice_col<VEC>(s, lane, k);
-          if (c < P.dim) v[u][k] = load_vec<TS, VEC>(src + t * P.dim + c);
+          if (c < P.dim) v[u][k] = load_global<TS, VEC>(src + t * P.dim + c);
         }
       }
     }
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) row_sums_join(const SumParams 
 #pragma unroll
           for (int k = 0; k < kK; ++k) {
             const int c = slice_col<VEC>(s, lane, k);
-            if (c < P.dim) v[u][k] = load_vec<float, VEC>(row + c);
+            if (c < P.dim) v[u][k] = load_global<float, VEC>(row + c);
           }
         }
 #pragma unroll

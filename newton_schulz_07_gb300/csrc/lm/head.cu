@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(256)
     const Vec<bf16, 8> w = load_vec<bf16, 8>(W + t * R.dim + c);
 #pragma unroll 4
     for (int s = 0; s < splits; ++s) {
-      const Vec<float, 8> v = load_vec<float, 8>(part + (s * rows + p) * R.dim + c);
+      const Vec<float, 8> v = load_global<float, 8>(part + (s * rows + p) * R.dim + c);
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] += v.v[j];
     }
