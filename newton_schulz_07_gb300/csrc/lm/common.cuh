@@ -185,6 +185,17 @@ inline int status_of(cudaError_t e) {
   return MUON_NS_ERR_CUDA;
 }
 
+// Allows `kernel` as much dynamic shared memory, once per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>* configured) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (configured->load() >> (dev & 63) & 1ull)) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) configured->fetch_or(1ull << (dev & 63));
+  return e;
+}
+
 // SMs of the current device (queried once per device).
 int sm_count();
 

@@ -6,15 +6,16 @@
 // Gradient: dE[v] = s sum_{ids[t] = v} dY[t].  Atomics would give a sum whose
 // order changes from run to run and would serialise on frequent tokens, so the
 // tokens are sorted by id first:
-//   token_sort     one cluster sorts (id, token) pairs by radix, stable, so a
-//                  row's tokens follow one another in token order, and marks
-//                  the ids that occur in a bitmap;
-//   row_sums       a warp takes kPiece sorted positions and 256 columns, adds
-//                  the rows in fp32 registers and writes a row of dE where it
-//                  ends inside the piece; a row that crosses pieces leaves one
-//                  partial row in each.  Other warps zero the rows of the ids
-//                  that do not occur, so dE is written once;
-//   row_sums_join  adds the partial rows of a row in piece order.
+//   token_rank,   up to 4096 tokens: each token's place is the number of smaller
+//   token_sort    ones, counted by all SMs; more: one cluster sorts (id, token)
+//                 pairs by radix.  Both stable, so a row's tokens follow one
+//                 another in token order.  The other CTAs of the launch zero
+//                 the rows of dE that no token names, so dE is written once;
+//   row_sums      a warp takes a piece of 8 or 32 sorted positions and 256 columns, adds
+//                 the rows in fp32 registers and writes a row of dE where it
+//                 ends inside the piece; a row that crosses pieces leaves one
+//                 partial row in each;
+//   row_sums_join adds the partial rows of a row in piece order.
 // dY is read once and dE written once: bound by HBM traffic.
 #include <cmath>
 #include <type_traits>
@@ -72,28 +73,107 @@ constexpr int kMaxDigit = 9;            // bits a pass sorts by
 constexpr int kBins = 1 << kMaxDigit;
 constexpr int kSortWarps = 32;
 constexpr int kSortUnroll = 8;          // elements a thread loads at once
-constexpr int kSortCluster = 8;         // CTAs of the sort, at most
-constexpr int kSortTokens = 2048;       // tokens a CTA of it should have, at least
+// CTAs of the sort: 8, or 4 where the launch also zeroes rows, since clusters
+// of 8 leave a sixth of the SMs without a CTA (clusters of 4 a twentieth) and
+// the zeroing takes longer than the sort.
+constexpr int kSortAlone = 8, kSortBeside = 4;
 constexpr size_t kSortSmem = sizeof(int) * kSortWarps * kBins;
+constexpr unsigned int kZeroWindow = 1 << 17;  // rows whose presence a zeroing CTA holds at once
+static_assert(kZeroWindow / 8 <= kRankSmem && kZeroWindow / 8 <= kSortSmem, "presence bits");
 
-// One cluster.  Each CTA owns a contiguous part of the tokens and each warp a
-// contiguous part of that.  A pass counts digits per warp, turns the counts
-// into the first output position of each (digit, CTA, warp) in that order, and
-// writes every element to its warp's next position: stable, since a warp
-// takes its elements in order and match_any ranks the lanes of one digit.
+template <typename V>
+__device__ __forceinline__ void zero_row(uint8_t* row, long long bytes, int lane) {
+  for (long long c = lane * sizeof(V); c < bytes; c += 32 * sizeof(V)) *reinterpret_cast<V*>(row + c) = V{};
+}
+
+// CTA `cta` of `ctas` (1024 threads): zeroes, of rows cta, cta + ctas, ..., those
+// that no token names, as its own reading of the ids says.  (Rows in turn, not
+// in parts: frequent ids lie together.)
+__device__ __forceinline__ void zero_absent(const SortBy& by, const ZeroRows& zero, int cta, int ctas, unsigned int* bits) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const unsigned int n = static_cast<unsigned int>((by.vocab - cta + ctas - 1) / ctas);  // rows of this CTA
+  const unsigned int inverse = 0xFFFFFFFFu / static_cast<unsigned int>(ctas);
+  uint8_t* table = static_cast<uint8_t*>(zero.table);
+  const long long rb = zero.row_bytes;
+  const unsigned long long step = static_cast<unsigned long long>(rb) | reinterpret_cast<uintptr_t>(table);
+  for (unsigned int a = 0; a < n; a += kZeroWindow) {
+    const unsigned int m = n - a < kZeroWindow ? n - a : kZeroWindow;
+    for (unsigned int i = tid; i < (m + 31) / 32; i += 1024) bits[i] = 0u;
+    __syncthreads();
+#pragma unroll 8
+    for (long long t = tid; t < by.tokens; t += 1024) {
+      const unsigned int key = sort_key(by, t);
+      // key / ctas and the remainder, from a quotient that may be a few short.
+      unsigned int q = __umulhi(key, inverse), r = key - q * ctas;
+      while (r >= static_cast<unsigned int>(ctas)) {
+        ++q;
+        r -= ctas;
+      }
+      if (r == static_cast<unsigned int>(cta) && q - a < m) {
+        // Frequent ids find their bit set: no queue of atomics on one word.
+        const unsigned int i = q - a, bit = 1u << (i & 31);
+        if (!(*static_cast<volatile unsigned int*>(&bits[i >> 5]) & bit)) atomicOr(&bits[i >> 5], bit);
+      }
+    }
+    __syncthreads();
+    for (unsigned int i = warp; i < m; i += 32) {
+      if ((bits[i >> 5] >> (i & 31)) & 1u) continue;
+      uint8_t* row = table + (static_cast<long long>(a + i) * ctas + cta) * rb;
+      if ((step & 31) == 0) {
+        const float z[8] = {};
+#pragma unroll 4
+        for (long long c = lane * 32; c < rb; c += 1024) store_global<float, 8>(reinterpret_cast<float*>(row + c), z);
+      } else if ((step & 15) == 0) {
+        zero_row<uint4>(row, rb, lane);
+      } else if ((step & 3) == 0) {
+        zero_row<unsigned int>(row, rb, lane);
+      } else {
+        zero_row<unsigned short>(row, rb, lane);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+__global__ void __launch_bounds__(1024)
+    token_rank(const SortBy by, const ZeroRows zero, int blocks, unsigned long long* __restrict__ sorted) {
+  extern __shared__ __align__(16) unsigned int keys[];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  if (static_cast<int>(blockIdx.x) >= blocks) {
+    zero_absent(by, zero, static_cast<int>(blockIdx.x) - blocks, static_cast<int>(gridDim.x) - blocks, keys);
+    return;
+  }
+  unsigned int key;
+  const int r = rank_tokens(by, blockIdx.x, keys, &key);
+  const long long t = static_cast<long long>(blockIdx.x) * kRankBlock + (threadIdx.x >> 5);
+  if ((threadIdx.x & 31) == 0 && t < by.tokens) sorted[r] = (static_cast<unsigned long long>(key) << 32) | t;
+}
+
+// The grid's first cluster sorts.  Each of its CTAs owns a contiguous part of
+// the tokens and each warp a contiguous part of that.  A pass counts digits per
+// warp, turns the counts into the first output position of each (digit, CTA,
+// warp) in that order, and writes every element to its warp's next position:
+// stable, since a warp takes its elements in order and match_any ranks the
+// lanes of one digit.
+template <int ctas>
 __global__ void __launch_bounds__(32 * kSortWarps)
-    token_sort(const void* __restrict__ ids, int ids64, long long tokens, long long vocab, const SortBy by, int passes,
-               int digit_bits, unsigned long long* buf_even, unsigned long long* buf_odd, unsigned int* bitmap,
-               long long words) {
-  extern __shared__ int cnt[];  // [kSortWarps][kBins]
+    token_sort(const SortBy by, const ZeroRows zero, int passes, int digit_bits, unsigned long long* buf_even,
+               unsigned long long* buf_odd) {
+  extern __shared__ __align__(16) unsigned int sort_smem[];  // counts, [kSortWarps][kBins]
   __shared__ int totals[kBins];
   __shared__ int base[kBins];
   __shared__ int scan_sh[kSortWarps];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int ctas = static_cast<int>(gridDim.x);  // the whole grid is one cluster
   const int rank = static_cast<int>(blockIdx.x);
+  if (rank >= ctas) {
+    zero_absent(by, zero, rank - ctas, static_cast<int>(gridDim.x) - ctas, sort_smem);
+    return;
+  }
+  int* cnt = reinterpret_cast<int*>(sort_smem);
+  const long long tokens = by.tokens;
   const long long per_cta = ((tokens + ctas - 1) / ctas + 31) / 32 * 32;
   const long long per_warp = ((per_cta + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
   const long long cta_begin = rank * per_cta;
@@ -102,13 +182,8 @@ __global__ void __launch_bounds__(32 * kSortWarps)
   const long long begin = cta_begin + warp * per_warp;
   long long end = begin + per_warp;
   if (end > cta_end) end = cta_end;
-  const long long none = by.presence ? 1 : vocab;  // key of an id that names no row
   const int bins = 1 << digit_bits;
   int* mine = cnt + warp * kBins;
-
-  for (long long i = static_cast<long long>(rank) * blockDim.x + tid; i < words;
-       i += static_cast<long long>(ctas) * blockDim.x)
-    bitmap[i] = 0u;
 
   for (int pass = 0; pass < passes; ++pass) {
     // Pass p writes buf_even if p is even; the last result is in the buffer
@@ -118,14 +193,12 @@ __global__ void __launch_bounds__(32 * kSortWarps)
     const int shift = 32 + pass * digit_bits;
     auto fetch = [&](long long i) -> unsigned long long {
       if (pass > 0) return __ldcg(src + i);
-      long long id = load_id(ids, ids64, i, vocab);
-      if (id == by.skip) id = -1;
-      if (by.presence && id >= 0) id = 0;
-      return (static_cast<unsigned long long>(id < 0 ? none : id) << 32) | static_cast<unsigned long long>(i);
+      return (static_cast<unsigned long long>(sort_key(by, i)) << 32) | static_cast<unsigned long long>(i);
     };
     for (int d = lane; d < bins; d += 32) mine[d] = 0;
     __syncwarp();
-    auto walk = [&](auto&& take) {
+    // f of the element of each position of the warp's part, in order.
+    auto walk = [&](auto&& f) {
       for (long long b = begin; b < end; b += 32 * kSortUnroll) {
         unsigned long long e[kSortUnroll];
 #pragma unroll
@@ -135,18 +208,13 @@ __global__ void __launch_bounds__(32 * kSortWarps)
         }
 #pragma unroll
         for (int u = 0; u < kSortUnroll; ++u) {
-          const long long i = b + u * 32 + lane;
-          const bool live = i < end;
-          const int d = live ? static_cast<int>((e[u] >> shift) & static_cast<unsigned>(bins - 1)) : kBins;
-          const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
-          const int before = __popc(same & ((1u << lane) - 1u));
-          take(live, d, before, __popc(same), e[u]);
-          __syncwarp();
+          const bool live = b + u * 32 + lane < end;
+          f(live, live ? static_cast<int>((e[u] >> shift) & static_cast<unsigned>(bins - 1)) : kBins, e[u]);
         }
       }
     };
-    walk([&](bool live, int d, int before, int n, unsigned long long) {
-      if (live && before == 0) mine[d] += n;
+    walk([&](bool live, int d, unsigned long long) {
+      if (live) atomicAdd(&mine[d], 1);
     });
     __syncthreads();
     // Counts -> offsets of each warp inside its CTA, and the CTA's totals.
@@ -161,17 +229,13 @@ __global__ void __launch_bounds__(32 * kSortWarps)
       totals[tid] = run;
     }
     __syncthreads();
-    if (ctas > 1) ptx::cluster_sync();
+    ptx::cluster_sync();
     int before_cta = 0, all = 0;
     if (tid < bins) {
       for (int r = 0; r < ctas; ++r) {
         int c;
-        if (ctas > 1) {
-          const uint32_t a = ptx::mapa(ptx::smem_u32(&totals[tid]), static_cast<uint32_t>(r));
-          asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(a) : "memory");
-        } else {
-          c = totals[tid];
-        }
+        const uint32_t a = ptx::mapa(ptx::smem_u32(&totals[tid]), static_cast<uint32_t>(r));
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(a) : "memory");
         if (r < rank) before_cta += c;
         all += c;
       }
@@ -197,29 +261,27 @@ __global__ void __launch_bounds__(32 * kSortWarps)
     __syncthreads();
     if (tid < bins) base[tid] = incl - all + (warp > 0 ? scan_sh[warp - 1] : 0) + before_cta;
     __syncthreads();
-    walk([&](bool live, int d, int before, int n, unsigned long long e) {
-      if (live) dst[base[d] + mine[d] + before] = e;
+    walk([&](bool live, int d, unsigned long long e) {
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
+      const int before = __popc(same & ((1u << lane) - 1u));
+      const int at = live ? mine[d] : 0;
       __syncwarp();
-      if (live && before == 0) mine[d] += n;
+      if (live && before == 0) mine[d] = at + __popc(same);
+      if (live) dst[base[d] + at + before] = e;
+      __syncwarp();
     });
     // The pass's writes are read by every CTA; totals and counts are reused.
-    if (ctas > 1)
-      ptx::cluster_sync();
-    else
-      __syncthreads();
+    ptx::cluster_sync();
   }
-  if (words == 0 && by.count == nullptr) return;
+  if (by.count == nullptr) return;
   const unsigned long long* sorted = (passes & 1) ? buf_even : buf_odd;
+  const unsigned int none = static_cast<unsigned int>(none_of(by));
   for (long long i = static_cast<long long>(rank) * blockDim.x + tid; i < tokens;
        i += static_cast<long long>(ctas) * blockDim.x) {
-    const unsigned int k = static_cast<unsigned int>(__ldcg(sorted + i) >> 32);
-    const bool first = i == 0 || static_cast<unsigned int>(__ldcg(sorted + i - 1) >> 32) != k;
-    const bool live = k < none;
-    if (words > 0 && first && live) atomicOr(bitmap + (k >> 5), 1u << (k & 31));
-    if (by.count != nullptr) {
-      if (first && !live) *by.count = static_cast<int>(i);
-      if (live && i == tokens - 1) *by.count = static_cast<int>(tokens);
-    }
+    const bool live = static_cast<unsigned int>(__ldcg(sorted + i) >> 32) < none;
+    if (!live && (i == 0 || static_cast<unsigned int>(__ldcg(sorted + i - 1) >> 32) < none))
+      *by.count = static_cast<int>(i);
+    if (live && i == tokens - 1) *by.count = static_cast<int>(tokens);
   }
 }
 
@@ -227,18 +289,19 @@ __global__ void __launch_bounds__(32 * kSortWarps)
 
 constexpr int kSliceCols = 256;  // columns of a warp: 8 a lane
 constexpr int kSumWarps = 8;
-constexpr int kSumUnroll = 8;    // rows a warp has in flight
-constexpr int kZeroRows = 8;     // table rows a zeroing warp looks after
+// Rows a warp has in flight.  (65536 tokens x 2048 bf16 take 88 us; 16 rows
+// leave fewer warps an SM and take half as long again.)
+constexpr int kSumUnroll = 8;
 
 struct SumParams {
   const void* src;
   void* out;
   const unsigned long long* sorted;
-  const unsigned int* bitmap;
   float* partial;  // [pieces][2][dim]: the row that began before the piece, the one that goes on after it
   const float* coef;  // COMPACT: factor of each sorted position
   int* slot;          // COMPACT
   long long tokens, vocab, pieces;
+  int piece;  // sorted positions of a piece, at most 32
   int dim, slices, accumulate;
   float scale;
 };
@@ -281,25 +344,15 @@ __global__ void __launch_bounds__(32 * kSumWarps) row_sums(const SumParams P) {
   const long long item = static_cast<long long>(blockIdx.x) * kSumWarps + (threadIdx.x >> 5);
   const long long sums = P.pieces * P.slices;
   TO* out = static_cast<TO*>(P.out);
-  if (item >= sums) {
-    if (COMPACT || P.accumulate) return;
-    // Rows of ids that do not occur.
-    const long long v0 = (item - sums) * kZeroRows;
-    if (v0 >= P.vocab) return;
-    const unsigned int bits = P.bitmap[v0 >> 5] >> (v0 & 31);
-    const float zero[VEC] = {};
-    for (int r = 0; r < kZeroRows; ++r)
-      if (v0 + r < P.vocab && !((bits >> r) & 1u))
-        for (int c = lane * VEC; c < P.dim; c += 32 * VEC) store_global<TO, VEC>(out + (v0 + r) * P.dim + c, zero);
-    return;
-  }
+  if (item >= sums) return;
   const long long piece = item / P.slices;
   const int s = static_cast<int>(item - piece * P.slices);
-  const long long p0 = piece * kPiece;
-  const int n = static_cast<int>(P.tokens - p0 < kPiece ? P.tokens - p0 : kPiece);
+  const long long p0 = piece * P.piece;
+  const int n = static_cast<int>(P.tokens - p0 < P.piece ? P.tokens - p0 : P.piece);
   const unsigned int none = static_cast<unsigned int>(P.vocab);
   const unsigned long long e = lane < n ? P.sorted[p0 + lane] : (static_cast<unsigned long long>(none) << 32);
   const unsigned int key = key_of(e);
+  const float coef = COMPACT && lane < n ? P.coef[p0 + lane] : 1.0f;
   // The keys around the piece, `none` past the ends.
   const unsigned int prev = p0 > 0 ? key_of(P.sorted[p0 - 1]) : none;
   const unsigned int next = p0 + n < P.tokens ? key_of(P.sorted[p0 + n]) : none;
@@ -331,7 +384,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) row_sums(const SumParams P) {
       const unsigned int ku = __shfl_sync(0xFFFFFFFFu, key, p);
       if (ku == none) continue;
       float f = 1.0f;
-      if (COMPACT) f = P.coef[p0 + p];
+      if (COMPACT) f = __shfl_sync(0xFFFFFFFFu, coef, p);
 #pragma unroll
       for (int k = 0; k < kK; ++k)
         if (slice_col<VEC>(s, lane, k) < P.dim)
@@ -359,86 +412,95 @@ __global__ void __launch_bounds__(32 * kSumWarps) row_sums(const SumParams P) {
   }
 }
 
-// A CTA looks at kSumWarps pieces; for each whose last row begins in it and
-// goes on, the CTA's warps add that row's partial rows, each a contiguous part
-// of the pieces, and the warps' sums are added in order.
+constexpr int kShortRun = 12;  // pieces of a row that one warp joins
+
+// Sum over pieces [b, e) of a row's partial rows, `first` being the piece it
+// began in.
+template <int VEC>
+__device__ __forceinline__ void add_pieces(const SumParams& P, long long b, long long e, long long first, int s,
+                                           int lane, float (&a)[8 / VEC][VEC]) {
+  constexpr int kK = 8 / VEC;
+  for (long long q0 = b; q0 < e; q0 += 4) {
+    Vec<float, VEC> v[4][kK];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (q0 + u < e) {
+        const float* row = P.partial + ((q0 + u) * 2 + (q0 + u == first ? 1 : 0)) * P.dim;
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          const int c = slice_col<VEC>(s, lane, k);
+          if (c < P.dim) v[u][k] = load_global<float, VEC>(row + c);
+        }
+      }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (q0 + u < e)
+#pragma unroll
+        for (int k = 0; k < kK; ++k)
+          if (slice_col<VEC>(s, lane, k) < P.dim)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) a[k][j] += v[u][k].v[j];
+  }
+}
+
+// A warp looks at a piece: if its last row begins in it and goes on, the row's
+// partial rows are added in order, by the warp where they are few, else by the
+// CTA's warps, each a contiguous part of them, and the warps' sums in order.
 template <typename TO, int VEC, bool COMPACT>
 __global__ void __launch_bounds__(32 * kSumWarps) row_sums_join(const SumParams P) {
   constexpr int kK = 8 / VEC;
   __shared__ float red[kSumWarps][kSliceCols];
-  __shared__ long long first_sh[kSumWarps], last_sh[kSumWarps];
-  __shared__ unsigned int key_sh[kSumWarps];
-  __shared__ int at_sh[kSumWarps];
+  __shared__ long long last_sh[kSumWarps], row_sh[kSumWarps];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = blockIdx.y;
   const unsigned int none = static_cast<unsigned int>(P.vocab);
-  const long long piece = static_cast<long long>(blockIdx.x) * kSumWarps + warp;
-  long long lo = 0, hi = 0;
-  unsigned int key = none;
-  int at = 0;
+  const long long first0 = static_cast<long long>(blockIdx.x) * kSumWarps;
+  const long long piece = first0 + warp;
+  TO* out = static_cast<TO*>(P.out);
+  long long last = -1;  // last piece of a row for the CTA to join
   if (piece + 1 < P.pieces) {
-    const long long p0 = piece * kPiece;
-    const unsigned int k = key_of(P.sorted[p0 + lane]);
-    key = __shfl_sync(0xFFFFFFFFu, k, 31);
-    // Positions of this piece in the run, and whether it began in the piece.
-    const unsigned int same = __ballot_sync(0xFFFFFFFFu, k == key);
-    at = __ffs(same) - 1;
-    const bool began = at > 0 || p0 == 0 || key_of(P.sorted[p0 - 1]) != key;
-    if (key != none && began && key_of(P.sorted[p0 + kPiece]) == key) {
-      // Last piece of the run: 32 probes a turn between lo (in the run) and hi.
-      lo = piece + 1;
-      hi = P.pieces;
+    const long long p0 = piece * P.piece;
+    const bool in_piece = lane < P.piece;
+    const unsigned int k = in_piece ? key_of(P.sorted[p0 + lane]) : none;
+    const unsigned int after = key_of(P.sorted[p0 + P.piece]);
+    const unsigned int prev = p0 > 0 ? key_of(P.sorted[p0 - 1]) : none;
+    const unsigned int key = __shfl_sync(0xFFFFFFFFu, k, P.piece - 1);
+    // The row's first position in this piece, and whether it began there.
+    const int at = __ffs(__ballot_sync(0xFFFFFFFFu, in_piece && k == key)) - 1;
+    if (key != none && after == key && (at > 0 || prev != key)) {
+      // Last piece of the row: 32 probes a turn between lo (in the row) and hi.
+      long long lo = piece + 1, hi = P.pieces;
+      long long step = 1;  // the next 32 pieces first: most rows end there
       while (hi - lo > 1) {
-        const long long step = (hi - lo + 31) / 32;
         const long long q = lo + (lane + 1) * step;
-        const bool in = q < hi && key_of(P.sorted[q * kPiece]) == key;
+        const bool in = q < hi && key_of(P.sorted[q * P.piece]) == key;
         const int ok = __popc(__ballot_sync(0xFFFFFFFFu, in));  // monotone
-        const long long nlo = lo + ok * step;
-        if (nlo + step < hi) hi = nlo + step;
-        lo = nlo;
+        lo += ok * step;
+        if (ok < 32 && lo + step < hi) hi = lo + step;
+        step = (hi - lo + 31) / 32;
       }
-    } else {
-      key = none;
+      const long long row = COMPACT ? p0 + at : static_cast<long long>(key);
+      if (lo - piece < kShortRun) {
+        float a[kK][VEC] = {};
+        add_pieces<VEC>(P, piece, lo + 1, piece, s, lane, a);
+        write_row<TO, VEC>(out + row * P.dim, s, lane, P.dim, P.scale, P.accumulate, a);
+      } else {
+        last = lo;
+        if (lane == 0) row_sh[warp] = row;
+      }
     }
   }
-  if (lane == 0) {
-    first_sh[warp] = piece;
-    last_sh[warp] = lo;
-    key_sh[warp] = key;
-    at_sh[warp] = at;
-  }
-  __syncthreads();
+  if (lane == 0) last_sh[warp] = last;
+  if (!__syncthreads_or(last >= 0 ? 1 : 0)) return;
   for (int w = 0; w < kSumWarps; ++w) {
-    if (key_sh[w] == none) continue;
-    const long long first = first_sh[w], last = last_sh[w];
-    const long long count = last - first + 1;  // partial rows, two at least
-    const long long per = (count + kSumWarps - 1) / kSumWarps;
+    if (last_sh[w] < 0) continue;
+    const long long first = first0 + w, end = last_sh[w] + 1;
+    const long long per = (end - first + kSumWarps - 1) / kSumWarps;
     const long long b = first + warp * per;
-    const long long e = b + per < last + 1 ? b + per : last + 1;
     float a[kK][VEC] = {};
-    for (long long q0 = b; q0 < e; q0 += 4) {
-      Vec<float, VEC> v[4][kK];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (q0 + u < e) {
-          const float* row = P.partial + ((q0 + u) * 2 + (q0 + u == first ? 1 : 0)) * P.dim;
-#pragma unroll
-          for (int k = 0; k < kK; ++k) {
-            const int c = slice_col<VEC>(s, lane, k);
-            if (c < P.dim) v[u][k] = load_global<float, VEC>(row + c);
-          }
-        }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (q0 + u < e)
-#pragma unroll
-          for (int k = 0; k < kK; ++k)
-            if (slice_col<VEC>(s, lane, k) < P.dim)
-#pragma unroll
-              for (int j = 0; j < VEC; ++j) a[k][j] += v[u][k].v[j];
-    }
+    add_pieces<VEC>(P, b, b + per < end ? b + per : end, first, s, lane, a);
     __syncthreads();  // the last turn's sums have been read
 #pragma unroll
     for (int k = 0; k < kK; ++k)
@@ -451,8 +513,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) row_sums_join(const SumParams 
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
           for (int g = 1; g < kSumWarps; ++g) a[k][j] += red[g][(k * 32 + lane) * VEC + j];
-      const long long row = COMPACT ? first * kPiece + at_sh[w] : static_cast<long long>(key_sh[w]);
-      write_row<TO, VEC>(static_cast<TO*>(P.out) + row * P.dim, s, lane, P.dim, P.scale, P.accumulate, a);
+      write_row<TO, VEC>(out + row_sh[w] * P.dim, s, lane, P.dim, P.scale, P.accumulate, a);
     }
   }
 }
@@ -472,8 +533,7 @@ void sort_plan(long long largest, int* passes, int* digit) {
 
 template <typename TS, typename TO, int VEC, bool COMPACT>
 cudaError_t launch_sums(const SumParams& P, cudaStream_t stream) {
-  const long long zero = COMPACT || P.accumulate ? 0 : (P.vocab + kZeroRows - 1) / kZeroRows;
-  const long long items = P.pieces * P.slices + zero;
+  const long long items = P.pieces * P.slices;
   cudaError_t e = mns::launch_pdl(row_sums<TS, TO, VEC, COMPACT>,
                                   dim3(static_cast<unsigned>((items + kSumWarps - 1) / kSumWarps)),
                                   dim3(32 * kSumWarps), 0, stream, P);
@@ -489,11 +549,11 @@ SumParams sum_params(const void* src, long long tokens, long long vocab, int dim
   P.src = src;
   P.out = out;
   P.sorted = reinterpret_cast<const unsigned long long*>(ws + L.sorted);
-  P.bitmap = reinterpret_cast<const unsigned int*>(ws + L.bitmap);
   P.partial = reinterpret_cast<float*>(ws + L.partial);
   P.tokens = tokens;
   P.vocab = vocab;
   P.pieces = L.pieces;
+  P.piece = L.piece;
   P.dim = dim;
   P.slices = (dim + kSliceCols - 1) / kSliceCols;
   P.accumulate = accumulate;
@@ -514,43 +574,50 @@ bool ids_aligned(const void* ids, int ids_bits) {
 
 }  // namespace
 
-SumLayout sum_layout(long long tokens, long long vocab, int dim) {
+SumLayout sum_layout(long long tokens, int dim) {
   SumLayout L;
-  L.pieces = (tokens + kPiece - 1) / kPiece;
+  // Short pieces give few tokens more warps; long ones leave fewer partial
+  // rows.
+  L.piece = tokens <= kRankTokens ? 8 : 32;
+  L.pieces = (tokens + L.piece - 1) / L.piece;
   size_t off = 0;
   L.sorted = off;
   off = align_up(off + 8 * static_cast<size_t>(tokens), 256);
   L.other = off;
   off = align_up(off + 8 * static_cast<size_t>(tokens), 256);
-  L.bitmap = off;
-  off = align_up(off + 4 * static_cast<size_t>((vocab + 31) / 32), 256);
   L.partial = off;
   off = align_up(off + 8 * static_cast<size_t>(L.pieces) * dim, 256);
   L.total = off;
   return L;
 }
 
-cudaError_t launch_sort(const void* ids, int ids64, long long tokens, long long vocab, const SortBy& by, uint8_t* ws,
-                        const SumLayout& L, cudaStream_t stream) {
-  int passes, digit;
-  sort_plan(by.presence ? 1 : vocab, &passes, &digit);
-  int ctas = 1;
-  while (ctas < kSortCluster && static_cast<long long>(ctas) * kSortTokens < tokens) ctas *= 2;
+cudaError_t launch_sort(const SortBy& by, const ZeroRows& zero, uint8_t* ws, const SumLayout& L, cudaStream_t stream) {
   auto* last = reinterpret_cast<unsigned long long*>(ws + L.sorted);
   auto* other = reinterpret_cast<unsigned long long*>(ws + L.other);
-  static std::atomic<unsigned long long> configured{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (!(configured.load() >> (dev & 63) & 1ull)) {
-    e = cudaFuncSetAttribute(token_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSortSmem));
-    if (e != cudaSuccess) return e;
-    configured.fetch_or(1ull << (dev & 63));
+  const int sms = sm_count();
+  if (by.tokens <= kRankTokens) {
+    const int blocks = static_cast<int>((by.tokens + kRankBlock - 1) / kRankBlock);
+    // Zeroing CTAs: two fit an SM.
+    const int zeros = zero.table == nullptr ? 0 : static_cast<int>(by.vocab < 2 * sms ? by.vocab : 2 * sms);
+    return mns::launch_pdl(token_rank, dim3(blocks + zeros), dim3(1024), kRankSmem, stream, by, zero, blocks, last);
   }
-  return mns::launch_pdl_cluster(token_sort, dim3(ctas), dim3(32 * kSortWarps), kSortSmem, stream, ctas, ids, ids64,
-                                 tokens, vocab, by, passes, digit, (passes & 1) ? last : other,
-                                 (passes & 1) ? other : last, reinterpret_cast<unsigned int*>(ws + L.bitmap),
-                                 by.presence ? 0 : (vocab + 31) / 32);
+  int passes, digit;
+  sort_plan(none_of(by), &passes, &digit);
+  unsigned long long *even = (passes & 1) ? last : other, *odd = (passes & 1) ? other : last;
+  static std::atomic<unsigned long long> configured[2];
+  if (zero.table == nullptr) {
+    const cudaError_t e = allow_smem(token_sort<kSortAlone>, static_cast<int>(kSortSmem), &configured[0]);
+    if (e != cudaSuccess) return e;
+    return mns::launch_pdl_cluster(token_sort<kSortAlone>, dim3(kSortAlone), dim3(32 * kSortWarps), kSortSmem, stream,
+                                   kSortAlone, by, zero, passes, digit, even, odd);
+  }
+  const cudaError_t e = allow_smem(token_sort<kSortBeside>, static_cast<int>(kSortSmem), &configured[1]);
+  if (e != cudaSuccess) return e;
+  // One CTA fits an SM; a twentieth of the SMs stays without a cluster.
+  const int clusters = sms * 19 / 20 / kSortBeside;
+  return mns::launch_pdl_cluster(token_sort<kSortBeside>, dim3(kSortBeside * (clusters < 2 ? 2 : clusters)),
+                                 dim3(32 * kSortWarps), kSortSmem, stream, kSortBeside, by, zero, passes, digit, even,
+                                 odd);
 }
 
 cudaError_t launch_row_sums(const void* src, int src_type, long long tokens, long long vocab, int dim, float scale,
@@ -618,7 +685,7 @@ int muon_embed_grad_workspace_size(long long tokens, long long vocab, int dim, s
   const int s = check(tokens, vocab, dim, 32);
   if (s != MUON_NS_OK) return s;
   if (!bytes) return MUON_NS_ERR_INVALID_ARG;
-  *bytes = tokens == 0 || vocab == 0 || dim == 0 ? 0 : sum_layout(tokens, vocab, dim).total;
+  *bytes = tokens == 0 || vocab == 0 || dim == 0 ? 0 : sum_layout(tokens, dim).total;
   return MUON_NS_OK;
 }
 
@@ -635,13 +702,15 @@ int muon_embed_grad(const void* dy, int dy_type, const void* ids, int ids_bits, 
   const size_t table_bytes = static_cast<size_t>(vocab) * dim * type_size(dtable_type);
   if (tokens > 0 && overlap(dy, static_cast<size_t>(tokens) * dim * type_size(dy_type), dtable, table_bytes))
     return MUON_NS_ERR_INVALID_ARG;
-  const SumLayout L = sum_layout(tokens, vocab, dim);
+  const SumLayout L = sum_layout(tokens, dim);
   if (tokens > 0 && (!workspace || workspace_bytes < L.total)) return MUON_NS_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MUON_NS_ERR_ALIGNMENT;
   if ((s = muon_ns_device_supported(-1)) != MUON_NS_OK) return s;
   if (tokens == 0) return accumulate ? MUON_NS_OK : status_of(cudaMemsetAsync(dtable, 0, table_bytes, stream));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  cudaError_t e = launch_sort(ids, ids_bits == 64 ? 1 : 0, tokens, vocab, SortBy{-1, 0, nullptr}, ws, L, stream);
+  const SortBy by = {ids, ids_bits == 64 ? 1 : 0, tokens, vocab, -1, 0, nullptr};
+  const ZeroRows zero = {accumulate ? nullptr : dtable, static_cast<long long>(dim) * type_size(dtable_type)};
+  const cudaError_t e = launch_sort(by, zero, ws, L, stream);
   if (e != cudaSuccess) return status_of(e);
   return status_of(launch_row_sums(dy, dy_type, tokens, vocab, dim, scale, dtable, dtable_type, accumulate ? 1 : 0, ws,
                                    L, stream));

@@ -49,23 +49,30 @@ constexpr int kHeadPairs = 76;            // CTA pairs the splits are chosen for
 constexpr int kHeadGroup = 8;             // pair rows walked together
 constexpr long long kPieceBytes = 1LL << 32;  // e of one piece, at most, by default
 
-// Splits of the vocabulary in dh, by the 256 threads of a CTA: output tiles
-// alone may be too few for the pairs, or fill their last turn badly.  A turn
-// costs its k-blocks and an epilogue worth about 6 of them; the fewest splits
-// of least cost are taken, at most 4 tiles a pair in all and 8 k-blocks each at
-// least.
-__device__ int choose_splits(int tiles, int kb) {
-  __shared__ unsigned long long best;
-  if (threadIdx.x == 0) best = ~0ull;
-  __syncthreads();
-  for (int s = threadIdx.x + 1; s <= 4 * kHeadPairs; s += 256) {
-    if (s > 1 && (static_cast<long long>(s) * tiles > 4 * kHeadPairs || kb / s < 8)) break;
-    const long long turns = (static_cast<long long>(tiles) * s + kHeadPairs - 1) / kHeadPairs;
-    const unsigned long long cost = static_cast<unsigned long long>(turns * ((kb + s - 1) / s + 6));
-    atomicMin(&best, (cost << 16) | static_cast<unsigned long long>(s));
+constexpr int kSplitTiles = 16 * kHeadPairs;  // tiles of all splits of dh, at most
+
+// Splits of the vocabulary in dh, by all threads of a CTA: output tiles alone
+// may be too few for the pairs, or fill their last turn badly (256 tiles on 76
+// pairs take 4 turns for 3.4; in two halves 7 for 6.7).  A turn costs its
+// k-blocks and an epilogue worth about 6 of them; the fewest splits of least
+// cost are taken, of 8 k-blocks each at least.
+__device__ __forceinline__ int choose_splits(long long all_tiles, int kb) {
+  __shared__ unsigned int best_sh[32];
+  if (all_tiles >= kSplitTiles) return 1;
+  const int tiles = static_cast<int>(all_tiles);
+  // Cost and splits in one word (costs past 2^20 blocks are all the same).
+  unsigned int best = ~0u;
+  for (int s = threadIdx.x + 1; s * tiles <= kSplitTiles && (s == 1 || kb / s >= 8); s += blockDim.x) {
+    const int turns = (tiles * s + kHeadPairs - 1) / kHeadPairs;
+    const int cost = turns * ((kb + s - 1) / s + 6);
+    const unsigned int c = (static_cast<unsigned int>(cost < (1 << 20) ? cost : (1 << 20) - 1) << 11) | s;
+    best = c < best ? c : best;
   }
+  best = __reduce_min_sync(0xFFFFFFFFu, best);
+  if ((threadIdx.x & 31) == 0) best_sh[threadIdx.x >> 5] = best;
   __syncthreads();
-  return static_cast<int>(best & 0xFFFFu);
+  for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) best = best_sh[w] < best ? best_sh[w] : best;
+  return static_cast<int>(best & 2047u);
 }
 
 struct HeadRows {
@@ -82,30 +89,24 @@ struct HeadRows {
   float* coef;   // -g (s - e_t) / s
 };
 
-// Compact copy of the live tokens' h, and the target's logit of each: a warp a
-// row.  The first CTA clears the control words and chooses dh's splits.
-__global__ void __launch_bounds__(256)
-    head_prepare(const HeadRows R, const bf16* __restrict__ h, const bf16* __restrict__ W, bf16* __restrict__ hc,
-                 int pair_rows, int split_kb) {
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  const int count = R.ctl[kCtlCount];
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < pair_rows; i += 256) R.redo[i] = 0;
-    const long long tiles = static_cast<long long>(token_pairs(count)) * ((R.dim + kHeadRows - 1) / kHeadRows);
-    const int splits = tiles > 4 * kHeadPairs ? 1 : choose_splits(static_cast<int>(tiles), split_kb);
-    if (threadIdx.x == 0) {
-      R.ctl[kCtlErr] = 0;
-      R.ctl[kCtlRedo] = 0;
-      R.ctl[kCtlSplits] = splits;
-    }
+// Clears the control words and chooses dh's splits: one CTA, all threads.
+__device__ __forceinline__ void start_call(const HeadRows& R, int count, int pair_rows, int split_kb) {
+  for (int i = threadIdx.x; i < pair_rows; i += blockDim.x) R.redo[i] = 0;
+  const int splits =
+      choose_splits(static_cast<long long>(token_pairs(count)) * ((R.dim + kHeadRows - 1) / kHeadRows), split_kb);
+  if (threadIdx.x == 0) {
+    R.ctl[kCtlErr] = 0;
+    R.ctl[kCtlRedo] = 0;
+    R.ctl[kCtlSplits] = splits;
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long p = static_cast<long long>(blockIdx.x) * 8 + warp;
-  if (p >= count) return;
-  const unsigned int token = static_cast<unsigned int>(R.sorted[p]);
+}
+
+// Row p of the compact copy of h, and its target's logit: one warp.
+__device__ __forceinline__ void start_row(const HeadRows& R, const bf16* __restrict__ h, const bf16* __restrict__ W,
+                                          bf16* __restrict__ hc, long long p, long long token) {
+  const int lane = threadIdx.x & 31;
   const long long t = load_id(R.targets, R.ids64, token, R.vocab);
-  const bf16* hr = h + static_cast<long long>(token) * R.dim;
+  const bf16* hr = h + token * R.dim;
   const bf16* wr = W + t * R.dim;
   bf16* out = hc + p * R.dim;
   float a[8] = {};
@@ -121,6 +122,38 @@ __global__ void __launch_bounds__(256)
     R.zt[p] = z;
     R.ref[p] = z;
   }
+}
+
+// Up to kRankTokens tokens: a CTA ranks 32 and starts their rows.
+__global__ void __launch_bounds__(1024)
+    head_rank(const SortBy by, const HeadRows R, const bf16* __restrict__ h, const bf16* __restrict__ W,
+              bf16* __restrict__ hc, int pair_rows, int split_kb, unsigned long long* __restrict__ sorted) {
+  extern __shared__ __align__(16) unsigned int keys[];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  unsigned int key;
+  const int p = rank_tokens(by, blockIdx.x, keys, &key);
+  const long long t = static_cast<long long>(blockIdx.x) * kRankBlock + (threadIdx.x >> 5);
+  if (t < by.tokens) {
+    if ((threadIdx.x & 31) == 0) sorted[p] = (static_cast<unsigned long long>(key) << 32) | t;
+    if (key < none_of(by)) start_row(R, h, W, hc, p, t);
+  }
+  if (blockIdx.x == 0) {
+    __syncthreads();
+    start_call(R, *static_cast<volatile int*>(by.count), pair_rows, split_kb);
+  }
+}
+
+// More tokens, after their sort.
+__global__ void __launch_bounds__(256)
+    head_start(const HeadRows R, const bf16* __restrict__ h, const bf16* __restrict__ W, bf16* __restrict__ hc,
+               int pair_rows, int split_kb) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int count = R.ctl[kCtlCount];
+  if (blockIdx.x == 0) start_call(R, count, pair_rows, split_kb);
+  const long long p = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (p < count) start_row(R, h, W, hc, p, static_cast<unsigned int>(R.sorted[p]));
 }
 
 struct HeadFinish {
@@ -158,8 +191,16 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
       continue;
     }
     if (F.again && R.redo[p / kHeadRows] == 0) continue;
+    // Loaded before the sums are joined; all independent of one another.
+    const float zt = R.zt[p], c = R.ref[p];
+    const long long t = load_id(R.targets, R.ids64, token, R.vocab);
+    const float g = F.hs == nullptr ? 0.0f : F.dloss != nullptr ? F.dloss[token] : 1.0f / static_cast<float>(count);
+    const bool one = F.hs != nullptr && R.dim <= 1024;  // a vector a thread
+    Vec<bf16, 8> x = {};
+    if (one && tid * 8 < R.dim) x = load_vec<bf16, 8>(F.hc + p * R.dim + tid * 8);
     const float2* st = F.stat + p * F.halves;
     float mx = -INFINITY, s = 0.0f;
+#pragma unroll 4
     for (int i = tid; i < F.halves; i += 128) {
       const float2 v = st[i];
       mx = fmaxf(mx, v.x);
@@ -184,12 +225,9 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
       }
       continue;
     }
-    const float zt = R.zt[p], c = R.ref[p];
     if (tid == 0) F.loss[token] = logf(s) + (c - zt);
     if (F.hs == nullptr) continue;
-    const float g = F.dloss != nullptr ? F.dloss[token] : 1.0f / static_cast<float>(count);
     const float f = g / s;
-    const long long t = load_id(R.targets, R.ids64, token, R.vocab);
     if (tid == 0) {
       R.scale[p] = f;
       R.coef[p] = -g * ((s - expf(zt - c)) / s);
@@ -198,7 +236,7 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
     // hs is the MMAs' bf16 operand: one more rounding, up to 2^-8, in each term of
     // dW but the targets', which are added in fp32.
     for (int col = tid * 8; col < R.dim; col += 1024) {
-      const Vec<bf16, 8> x = load_vec<bf16, 8>(F.hc + p * R.dim + col);
+      if (!one) x = load_vec<bf16, 8>(F.hc + p * R.dim + col);
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = f * to_f32(x.v[j]);
@@ -218,34 +256,59 @@ __global__ void __launch_bounds__(256)
   if (t >= v0 && t < v0 + vp) e[p * lde + (t - v0)] = 0;
 }
 
-// dh[token] = scale (sum of the splits) + coef W[target], 8 columns a thread.
+// dh[token] = scale (sum of the splits, in order) + coef W[target].  An item is
+// a row and 256 of its columns.  With many items a warp takes one; with few
+// (SHARED), where splits are many, a CTA's warps share one, a contiguous part of
+// the splits each.
+template <bool SHARED>
 __global__ void __launch_bounds__(256)
-    head_join_dh(const HeadRows R, const float* __restrict__ part, const bf16* __restrict__ W, bf16* __restrict__ dh) {
+    head_join_dh(const HeadRows R, const float* __restrict__ part, const bf16* __restrict__ W, bf16* __restrict__ dh,
+                 int slices) {
+  __shared__ float red[SHARED ? 8 : 1][256];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int count = R.ctl[kCtlCount], splits = R.ctl[kCtlSplits];
   const long long rows = static_cast<long long>(token_pairs(count)) * kHeadRows;
-  const int per = R.dim / 8;
-  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  const long long p = i / per;
-  if (p >= R.tokens) return;
-  const int c = static_cast<int>(i - p * per) * 8;
-  const unsigned int token = static_cast<unsigned int>(R.sorted[p]);
-  float o[8] = {};
-  if (p < count) {
-    const long long t = load_id(R.targets, R.ids64, token, R.vocab);
-    const Vec<bf16, 8> w = load_vec<bf16, 8>(W + t * R.dim + c);
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
+  const long long items = R.tokens * slices;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto add = [&](long long p, int c, int s0, int s1, float (&o)[8]) {
+#pragma unroll 8
+    for (int s = s0; s < s1; ++s) {
       const Vec<float, 8> v = load_global<float, 8>(part + (s * rows + p) * R.dim + c);
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] += v.v[j];
     }
-    const float f = R.scale[p], k = R.coef[p];
+  };
+  auto finish = [&](long long p, int c, const float (&o)[8]) {
+    const unsigned int token = static_cast<unsigned int>(R.sorted[p]);
+    float out[8] = {};
+    if (p < count) {
+      const long long t = load_id(R.targets, R.ids64, token, R.vocab);
+      const Vec<bf16, 8> w = load_vec<bf16, 8>(W + t * R.dim + c);
+      const float f = R.scale[p], k = R.coef[p];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = fmaf(f, o[j], k * to_f32(w.v[j]));
+      for (int j = 0; j < 8; ++j) out[j] = fmaf(f, o[j], k * to_f32(w.v[j]));
+    }
+    store_vec<bf16, 8>(dh + static_cast<long long>(token) * R.dim + c, out);
+  };
+  const long long i = SHARED ? blockIdx.x : static_cast<long long>(blockIdx.x) * 8 + warp;
+  if (i >= items) return;
+  const long long p = i / slices;
+  const int c = static_cast<int>(i - p * slices) * 256 + lane * 8;
+  const bool live = p < count && c < R.dim;
+  float o[8] = {};
+  if (live) add(p, c, SHARED ? splits * warp / 8 : 0, SHARED ? splits * (warp + 1) / 8 : splits, o);
+  if (SHARED) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) red[warp][j * 32 + lane] = o[j];
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int g = 1; g < 8; ++g)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] += red[g][j * 32 + lane];
   }
-  store_vec<bf16, 8>(dh + static_cast<long long>(token) * R.dim + c, o);
+  if (c < R.dim) finish(p, c, o);
 }
 
 // -------------------------------------------------------------------- host --
@@ -291,7 +354,7 @@ HeadLayout head_layout(long long tokens, long long vocab, int dim, bool grad, in
   L.scale = take(4 * n_tok);
   L.coef = take(4 * n_tok);
   L.stat = take(8 * n_tok * L.halves);
-  L.sum = grad ? sum_layout(tokens, vocab, dim) : sum_layout(tokens, 0, 0);
+  L.sum = sum_layout(tokens, grad ? dim : 0);
   L.sums = take(L.sum.total);
   L.hc = take(2 * n_tok * dim);
   if (grad) {
@@ -300,9 +363,9 @@ HeadLayout head_layout(long long tokens, long long vocab, int dim, bool grad, in
     L.addend = take(4 * n_tok * dim);
     L.e = take(2 * n_tok * static_cast<size_t>(L.lde));
     // Rows of the splits: choose_splits takes one, or as many as make at most
-    // 4 kHeadPairs tiles.
+    // kSplitTiles tiles.
     const long long tn = (dim + kHeadRows - 1) / kHeadRows;
-    long long rows = 4 * kHeadPairs / tn;
+    long long rows = kSplitTiles / tn;
     if (rows < pair_rows) rows = pair_rows;
     L.part_rows = rows * kHeadRows;
     L.part = take(4 * static_cast<size_t>(L.part_rows) * dim);
@@ -403,13 +466,20 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
   bf16* hs = reinterpret_cast<bf16*>(at(L.hs));
   bf16* e = reinterpret_cast<bf16*>(at(L.e));
 
-  MNS_TRY(launch_sort(C.targets, C.ids64, N, V, SortBy{C.skip, grad ? 0 : 1, R.ctl + kCtlCount}, at(L.sums), L.sum,
-                      C.stream));
   auto width = [&](long long j) { return V - j * L.piece < L.piece ? V - j * L.piece : L.piece; };
   // Splits are the same for every piece: chosen for the shortest.
   const int split_kb = static_cast<int>((width(L.pieces - 1) + kBlockK - 1) / kBlockK);
-  MNS_TRY(mns::launch_pdl(head_prepare, dim3(static_cast<unsigned>((N + 7) / 8)), dim3(256), 0, C.stream, R, C.h, C.W,
-                          hc, static_cast<int>(pair_rows), split_kb));
+  // The losses alone need no order among the live tokens.
+  const SortBy by = {C.targets, C.ids64, N, V, C.skip, grad ? 0 : 1, R.ctl + kCtlCount};
+  if (N <= kRankTokens) {
+    MNS_TRY(mns::launch_pdl(head_rank, dim3(static_cast<unsigned>((N + kRankBlock - 1) / kRankBlock)), dim3(1024),
+                            kRankSmem, C.stream, by, R, C.h, C.W, hc, static_cast<int>(pair_rows), split_kb,
+                            reinterpret_cast<unsigned long long*>(at(L.sums + L.sum.sorted))));
+  } else {
+    MNS_TRY(launch_sort(by, ZeroRows{nullptr, 0}, at(L.sums), L.sum, C.stream));
+    MNS_TRY(mns::launch_pdl(head_start, dim3(static_cast<unsigned>((N + 7) / 8)), dim3(256), 0, C.stream, R, C.h, C.W,
+                            hc, static_cast<int>(pair_rows), split_kb));
+  }
 
   HeadGemm G = {};
   G.ctl = R.ctl;
@@ -475,15 +545,14 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
     if (!map2d(&P.tmA, e, vp, N, L.lde, kBlockK, kTileM) || !map2d(&P.tmB, C.W + v0 * D, D, vp, D, 64, kBlockK) ||
         !map2d(&P.tmOut, at(L.part), D, L.part_rows, D, 32, 32, true))
       return MUON_NS_ERR_CUDA;
-    // At most one tile a split more than choose_splits may take.
-    const long long most = pair_rows * dim_tiles > 4 * kHeadPairs ? pair_rows * dim_tiles : 4 * kHeadPairs;
+    const long long most = pair_rows * dim_tiles > kSplitTiles ? pair_rows * dim_tiles : kSplitTiles;
     MNS_TRY(launch_gemm<kDh>(P, most, C.stream));
     P = G;
     P.vp = vp;
     P.add = C.accumulate;
     P.addend = addend;
     P.slot = slot;
-    P.bitmap = reinterpret_cast<const unsigned int*>(at(L.sums + L.sum.bitmap));
+    P.sorted = R.sorted;
     P.v0 = v0;
     void* dst = static_cast<uint8_t*>(C.dW) + static_cast<size_t>(v0) * D * (C.dW_f32 ? 4 : 2);
     if (!map2d(&P.tmA, e, vp, N, L.lde, 64, kBlockK) || !map2d(&P.tmB, hs, D, N, D, 64, kBlockK) ||
@@ -492,9 +561,12 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
     const long long units = static_cast<long long>((vp + kHeadRows - 1) / kHeadRows) * dim_tiles;
     MNS_TRY(C.dW_f32 ? launch_gemm<kDwF32>(P, units, C.stream) : launch_gemm<kDwBf16>(P, units, C.stream));
   }
-  const long long vecs = N * (D / 8);
-  MNS_TRY(mns::launch_pdl(head_join_dh, dim3(static_cast<unsigned>((vecs + 255) / 256)), dim3(256), 0, C.stream, R,
-                          static_cast<const float*>(f32_at(L.part)), C.W, C.dh));
+  const int slices = static_cast<int>((D + 255) / 256);
+  const long long items = N * slices;
+  const bool shared = items <= 16LL * sm_count();
+  MNS_TRY(mns::launch_pdl(shared ? head_join_dh<true> : head_join_dh<false>,
+                          dim3(static_cast<unsigned>(shared ? items : (items + 7) / 8)), dim3(256), 0, C.stream, R,
+                          static_cast<const float*>(f32_at(L.part)), C.W, C.dh, slices));
   return MUON_NS_OK;
 }
 

@@ -63,8 +63,8 @@ struct HeadGemm {
   int add;
   // kDw*
   const float* addend;         // fp32 [rows][dim], compact
-  const int* slot;             // row of a vocabulary row's addend, where its bit is set
-  const unsigned int* bitmap;
+  const int* slot;             // row of a vocabulary row's addend: one if sorted[slot] has its key
+  const unsigned long long* sorted;
   long long v0;                // first vocabulary row of the piece
   long long budget;
 };
@@ -278,6 +278,20 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
     const uint32_t stg = smem_base + kHeadStages * kHeadStageBytes + static_cast<uint32_t>(e * kHeadStaging);
     int buf = 0;
     uint32_t tphase = 0;
+    // kDw*: the addend of this lane's row in unit u, or null.  The slot is
+    // read a unit ahead.
+    auto slot_of = [&](long long u) {
+      if (u >= total) return -1;
+      const int row = unit(u).I * kTileM + q * 32 + lane;
+      return row < P.vp ? P.slot[P.v0 + row] : -1;
+    };
+    auto addend_of = [&](const Unit& t, int slot) -> const float* {
+      const long long v = P.v0 + t.I * kTileM + q * 32 + lane;
+      if (static_cast<unsigned>(slot) >= static_cast<unsigned>(count)) return nullptr;
+      return (P.sorted[slot] >> 32) == static_cast<unsigned long long>(v) ? P.addend + static_cast<long long>(slot) * P.dim
+                                                                        : nullptr;
+    };
+    int slot_next = MODE >= kDwBf16 ? slot_of(unit0) : -1;
     for (long long u = unit0; u < total; u += ustride) {
       const Unit t = unit(u);
       if (skip(t)) continue;
@@ -293,9 +307,9 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
         if (live) cl = P.ref[row] * kLog2e;
       }
       const float* addend = nullptr;
-      if (MODE >= kDwBf16 && row < P.vp) {
-        const long long v = P.v0 + row;
-        if ((P.bitmap[v >> 5] >> (v & 31)) & 1u) addend = P.addend + static_cast<long long>(P.slot[v]) * P.dim;
+      if (MODE >= kDwBf16) {
+        addend = addend_of(t, slot_next);
+        slot_next = slot_of(u + ustride);
       }
       int ready = 0;
       if (lane == 0) ready = detail::wait_bounded<true>(tfull(buf), tphase, abort_flag, err, P.budget) ? 1 : 0;

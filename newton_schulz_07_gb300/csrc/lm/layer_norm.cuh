@@ -130,17 +130,6 @@ auto with_norm_vec(int vec, F&& f) {
   }
 }
 
-// Allows `kernel` as much dynamic shared memory, once per device.
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>* configured) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (configured->load() >> (dev & 63) & 1ull)) return e;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) configured->fetch_or(1ull << (dev & 63));
-  return e;
-}
-
 inline int norm_check(long long rows, int dim) {
   if (rows < 0 || dim < 0 || rows > kMaxRows || dim > kMaxDim) return MUON_NS_ERR_INVALID_ARG;
   if (rows > 0 && dim == 0) return MUON_NS_ERR_INVALID_ARG;

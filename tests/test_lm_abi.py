@@ -120,8 +120,8 @@ def test_valid_calls_without_a_device_are_unsupported():
 
 def test_workspace_sizes():
     assert ns.embed_grad_workspace_size(0, 10, 8) == 0 and ns.layer_norm_grad_workspace_size(0, 8) == 0
-    # Sorted pairs twice, the bitmap, two partial rows a piece of 32 positions.
-    assert ns.embed_grad_workspace_size(1000, 100, 64) >= 16 * 1000 + 4 * 4 + 32 * 2 * 64 * 4
+    # Sorted pairs twice, two partial rows a piece of 32 positions.
+    assert ns.embed_grad_workspace_size(1000, 100, 64) >= 16 * 1000 + 32 * 2 * 64 * 4
     assert ns.layer_norm_grad_workspace_size(1, 24) >= 2 * 24 * 4
     with pytest.raises(ns.MuonNSError):
         ns.embed_grad_workspace_size(-1, 10, 8)
