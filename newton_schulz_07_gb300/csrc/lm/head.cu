@@ -313,6 +313,8 @@ __global__ void __launch_bounds__(256)
 
 // -------------------------------------------------------------------- host --
 
+inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
 struct HeadLayout {
   size_t redo, zt, ref, scale, coef, stat, sums, slot, hc, hs, addend, e, part, total;
   SumLayout sum;
@@ -391,6 +393,7 @@ bool map2d(CUtensorMap* map, const void* base, long long inner, long long rows, 
 
 template <int MODE>
 cudaError_t launch_gemm(const HeadGemm& P, long long units, cudaStream_t stream) {
+  if (units >= (1LL << 30)) return cudaErrorInvalidValue;  // 32-bit tile numbers in the kernel
   static std::atomic<int> resident[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -496,9 +499,11 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
     P.store = store ? 1 : 0;
     P.redo = redo;
     if (!map2d(&P.tmA, hc, D, N, D, kBlockK, kTileM) ||
-        !map2d(&P.tmB, C.W + j * L.piece * D, D, P.vp, D, kBlockK, kTileN / 2) ||
-        (store && !map2d(&P.tmOut, e, P.vp, N, L.lde, 64, 32)))
+        !map2d(&P.tmB, C.W + j * L.piece * D, D, P.vp, D, kBlockK, kTileN / 2))
       return MUON_NS_ERR_CUDA;
+    P.out = e;
+    P.ld = L.lde;
+    P.rows = static_cast<int>(N);
     return status_of(launch_gemm<kLogits>(P, pair_rows * ((P.vp + kHeadRows - 1) / kHeadRows), C.stream));
   };
   const long long kept = L.pieces - 1;  // piece whose e the first pass leaves
@@ -556,8 +561,12 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
     P.v0 = v0;
     void* dst = static_cast<uint8_t*>(C.dW) + static_cast<size_t>(v0) * D * (C.dW_f32 ? 4 : 2);
     if (!map2d(&P.tmA, e, vp, N, L.lde, 64, kBlockK) || !map2d(&P.tmB, hs, D, N, D, 64, kBlockK) ||
-        !map2d(&P.tmOut, dst, D, vp, D, C.dW_f32 ? 32 : 64, 32, C.dW_f32 != 0))
+        (C.dW_f32 && !map2d(&P.tmOut, dst, D, vp, D, 32, 32, true)))
       return MUON_NS_ERR_CUDA;
+    P.out = dst;
+    P.ld = D;
+    P.rows = vp;
+    P.sectors = D % 16 == 0 && aligned(dst, 32) ? 1 : 0;
     const long long units = static_cast<long long>((vp + kHeadRows - 1) / kHeadRows) * dim_tiles;
     MNS_TRY(C.dW_f32 ? launch_gemm<kDwF32>(P, units, C.stream) : launch_gemm<kDwBf16>(P, units, C.stream));
   }
@@ -576,12 +585,6 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
 }  // namespace mns
 
 using namespace mns::lm;
-
-namespace {
-
-inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-}  // namespace
 
 extern "C" {
 

@@ -25,6 +25,7 @@
 #include <cuda.h>
 
 #include "gemm_tc.cuh"
+#include "lm/common.cuh"
 
 namespace mns {
 namespace lm {
@@ -53,6 +54,11 @@ struct HeadGemm {
   int vp;   // vocabulary columns of the piece
   int dim;
   int group;  // pair rows walked together, column by column
+  // kLogits (e) and kDwBf16 (dW): bf16 output, written from registers.
+  void* out;
+  long long ld;
+  int rows;     // rows of the output
+  int sectors;  // its rows start on 32 bytes
   // kLogits
   const float* ref;   // per row
   float2* stat;       // [rows][stat_ld]: (largest z, sum of e) of 128 columns; may be null
@@ -88,6 +94,42 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src,
                "r"(x), "r"(y), "r"(z), "r"(src)
                : "memory");
 }
+
+// Arrival on a barrier of the pair's other CTA that orders no memory: it tells
+// the MMA thread that an accumulator has been read, which tcgen05.wait::ld and
+// the fence before it have made sure of.  (A release at cluster scope waits for
+// every earlier write of the thread, about 2000 cycles a tile here.)
+__device__ __forceinline__ void arrive_remote_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// 16 bf16 to a 32-byte aligned address: one whole sector a lane.
+__device__ __forceinline__ void store_sector(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Division by a number known once per launch: a multiplication and at most two
+// corrections in place of the hundreds of cycles of a 64-bit division, which
+// each role would take between two tiles.
+struct FastDiv {
+  uint32_t d, m;
+  __device__ __forceinline__ explicit FastDiv(uint32_t divisor) : d(divisor), m(0xFFFFFFFFu / divisor) {}
+  __device__ __forceinline__ uint32_t operator()(uint32_t n, uint32_t* rest) const {
+    uint32_t q = __umulhi(n, m), r = n - q * d;
+    if (r >= d) {
+      ++q;
+      r -= d;
+    }
+    if (r >= d) {
+      ++q;
+      r -= d;
+    }
+    *rest = r;
+    return q;
+  }
+};
 
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -139,7 +181,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
     ptx::fence_barrier_init();
     ptx::prefetch_tensormap(&P.tmA);
     ptx::prefetch_tensormap(&P.tmB);
-    ptx::prefetch_tensormap(&P.tmOut);
+    if (MODE == kDh || MODE == kDwF32) ptx::prefetch_tensormap(&P.tmOut);
   }
   __syncthreads();
   ptx::cluster_sync();
@@ -161,20 +203,32 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
                      : MODE == kDh   ? (P.vp + kBlockK - 1) / kBlockK
                                      : (count > 0 ? (count + kBlockK - 1) / kBlockK : 1);
   const int splits = MODE == kDh ? P.ctl[kCtlSplits] : 1;
-  const long long tiles = static_cast<long long>(pr) * tn;
-  const long long total = tiles * splits;
-  const long long unit0 = ptx::cluster_id_x(), ustride = ptx::cluster_count_x();
+  // (Fewer than 2^31 tiles: the host sees to it.)
+  const uint32_t tiles = static_cast<uint32_t>(pr) * static_cast<uint32_t>(tn);
+  const uint32_t total = tiles * static_cast<uint32_t>(splits);
+  const uint32_t unit0 = ptx::cluster_id_x(), ustride = ptx::cluster_count_x();
+  const FastDiv by_tiles(tiles), by_group(static_cast<uint32_t>(P.group) * static_cast<uint32_t>(tn));
+  // A band of `group` pair rows is walked column by column; the last may hold
+  // fewer.
+  const FastDiv by_rows(P.group), by_last(pr % P.group ? pr % P.group : P.group);
+  const uint32_t last_band = static_cast<uint32_t>((pr - 1) / P.group);
   struct Unit {
     int I, J, s, kb0, kb1;  // row tile of this CTA, column tile, split, its k-blocks
   };
-  auto unit = [&](long long u) {
+  auto unit = [&](uint32_t u) {
     Unit t;
-    t.s = static_cast<int>(u / tiles);
-    int p;
-    grid_decode(u - t.s * tiles, pr, tn, &p, &t.J, P.group);
-    t.I = 2 * p + crank;
-    t.kb0 = static_cast<int>(static_cast<long long>(kb_all) * t.s / splits);
-    t.kb1 = static_cast<int>(static_cast<long long>(kb_all) * (t.s + 1) / splits);
+    uint32_t in_split = u, in_band, row;
+    t.s = 0;
+    t.kb0 = 0;
+    t.kb1 = kb_all;
+    if (MODE == kDh) {
+      t.s = static_cast<int>(by_tiles(u, &in_split));
+      t.kb0 = static_cast<int>(static_cast<long long>(kb_all) * t.s / splits);
+      t.kb1 = static_cast<int>(static_cast<long long>(kb_all) * (t.s + 1) / splits);
+    }
+    const uint32_t band = by_group(in_split, &in_band);
+    t.J = static_cast<int>(band == last_band ? by_last(in_band, &row) : by_rows(in_band, &row));
+    t.I = 2 * static_cast<int>(band * P.group + row) + crank;
     return t;
   };
   auto skip = [&](const Unit& t) { return MODE == kLogits && P.redo != nullptr && P.redo[t.I >> 1] == 0; };
@@ -186,7 +240,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
       int stage = 0, fills = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (long long u = unit0; ok && u < total; u += ustride) {
+      for (uint32_t u = unit0; ok && u < total; u += ustride) {
         const Unit t = unit(u);
         if (skip(t)) continue;
         const int row0 = t.I * kTileM, col0 = t.J * kTileN + crank * (kTileN / 2);
@@ -230,7 +284,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
       int stage = 0, buf = 0, stages = 0, units = 0;
       uint32_t phase = 0, tphase = 0;
       bool ok = true;
-      for (long long u = unit0; ok && u < total; u += ustride) {
+      for (uint32_t u = unit0; ok && u < total; u += ustride) {
         const Unit t = unit(u);
         if (skip(t)) continue;
         if (!detail::wait_bounded<true>(tempty(buf), tphase ^ 1u, abort_flag, err, P.budget)) break;
@@ -278,21 +332,26 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
     const uint32_t stg = smem_base + kHeadStages * kHeadStageBytes + static_cast<uint32_t>(e * kHeadStaging);
     int buf = 0;
     uint32_t tphase = 0;
-    // kDw*: the addend of this lane's row in unit u, or null.  The slot is
-    // read a unit ahead.
-    auto slot_of = [&](long long u) {
-      if (u >= total) return -1;
-      const int row = unit(u).I * kTileM + q * 32 + lane;
-      return row < P.vp ? P.slot[P.v0 + row] : -1;
+    // kDw*: where the addend of this lane's row is, resolved a tile ahead: the
+    // slot's load is issued two tiles ahead, that of the key it must have one.
+    auto row_of = [&](uint32_t u) {
+      const int row = u < total ? unit(u).I * kTileM + q * 32 + lane : P.vp;
+      return row < P.vp ? row : -1;
     };
-    auto addend_of = [&](const Unit& t, int slot) -> const float* {
-      const long long v = P.v0 + t.I * kTileM + q * 32 + lane;
-      if (static_cast<unsigned>(slot) >= static_cast<unsigned>(count)) return nullptr;
-      return (P.sorted[slot] >> 32) == static_cast<unsigned long long>(v) ? P.addend + static_cast<long long>(slot) * P.dim
-                                                                        : nullptr;
+    auto slot_at = [&](int row) { return row >= 0 ? P.slot[P.v0 + row] : -1; };
+    auto key_at = [&](int slot) {
+      return static_cast<unsigned>(slot) < static_cast<unsigned>(count) ? P.sorted[slot] >> 32 : ~0ull;
     };
-    int slot_next = MODE >= kDwBf16 ? slot_of(unit0) : -1;
-    for (long long u = unit0; u < total; u += ustride) {
+    int row1 = -1, slot1 = -1;          // next tile
+    int slot0 = -1;                     // this tile
+    unsigned long long key0 = ~0ull;
+    if (MODE >= kDwBf16) {
+      slot0 = slot_at(row_of(unit0));
+      key0 = key_at(slot0);
+      row1 = row_of(unit0 + ustride);
+      slot1 = slot_at(row1);
+    }
+    for (uint32_t u = unit0; u < total; u += ustride) {
       const Unit t = unit(u);
       if (skip(t)) continue;
       const int row_w = t.I * kTileM + q * 32;  // first row of the warp
@@ -308,8 +367,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
       }
       const float* addend = nullptr;
       if (MODE >= kDwBf16) {
-        addend = addend_of(t, slot_next);
-        slot_next = slot_of(u + ustride);
+        if (key0 == static_cast<unsigned long long>(P.v0 + row)) addend = P.addend + static_cast<long long>(slot0) * P.dim;
+        slot0 = slot1;
+        key0 = key_at(slot1);
+        row1 = row_of(u + 2 * ustride);
+        slot1 = slot_at(row1);
       }
       int ready = 0;
       if (lane == 0) ready = detail::wait_bounded<true>(tfull(buf), tphase, abort_flag, err, P.budget) ? 1 : 0;
@@ -319,6 +381,18 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
       ptx::tc_fence_after();
       const uint32_t t_lane =
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * kTileN + c_begin);
+      // The pair's next MMAs write both CTAs' accumulators: one arrival a warp,
+      // on CTA 0's barrier.
+      auto release = [&] {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader)
+            ptx::mbar_arrive(tempty(buf));
+          else
+            arrive_remote_relaxed(ptx::mapa(tempty(buf), 0));
+        }
+      };
       float mx = -INFINITY, s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
       for (int cc = 0; cc < kHeadHalf / 32; ++cc) {
@@ -327,6 +401,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
         uint32_t v[32];
         ptx::tmem_ld_32cols(t_lane + static_cast<uint32_t>(cc * 32), v);
         ptx::tmem_wait_ld();
+        if (cc + 1 == kHeadHalf / 32 || gj + 32 >= cols) {
+          // The warp's last read: its part of the accumulator may be written.
+          release();
+        }
         if (MODE == kLogits) {
           // Columns past the piece hold zero, not a logit: no part of the sums.
           const int n = cols - gj;
@@ -342,30 +420,17 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
             s4[j & 3] += f[j];
           }
           if (P.store) {
-            // Two chunks fill a box of 64 columns.  e is rounded to bf16 here,
-            // the MMAs' operand type: a relative error of up to 2^-8 in each term of
-            // sums over many; the target's term, which cancels, is left out of
-            // e and added in fp32.  Rows past the live tokens are zero.
-            const int h = cc & 1;
-            if (h == 0) {
-              if (lane == 0) ptx::bulk_wait_read<0>();
-              __syncwarp();
-            }
+            // e is rounded to bf16 here, the MMAs' operand type: a relative
+            // error of up to 2^-8 in each term of sums over many; the target's
+            // term, which cancels, is left out of e and added in fp32.  Rows
+            // past the live tokens are zero.
+            if (row < P.rows) {
+              uint32_t w[16];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = live ? detail::pack_bf16x2(f[8 * g + 2 * k], f[8 * g + 2 * k + 1]) : 0u;
-              ptx::st_shared_v4(stg + stage_off_wide(lane, h * 4 + g), w[0], w[1], w[2], w[3]);
-            }
-            if (h == 1 || gj + 32 >= cols) {
-              ptx::fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                ptx::tma_store_3d(&P.tmOut, stg, gj - h * 32, row_w, 0);
-                ptx::bulk_commit();
-              }
+              for (int k = 0; k < 16; ++k) w[k] = live ? detail::pack_bf16x2(f[2 * k], f[2 * k + 1]) : 0u;
+              bf16* to = static_cast<bf16*>(P.out) + static_cast<long long>(row) * P.ld + gj;
+              store_sector(to, w);
+              store_sector(to + 16, w + 8);
             }
           }
         } else {
@@ -385,23 +450,18 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
             }
           }
           if (MODE == kDwBf16) {
-            const int h = cc & 1;
-            if (h == 0) {
-              if (lane == 0) ptx::bulk_wait_read<0>();
-              __syncwarp();
-            }
+            if (row < P.rows) {
+              uint32_t w[16];
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-              ptx::st_shared_v4(stg + stage_off_wide(lane, h * 4 + g), detail::pack_bf16x2(f[8 * g], f[8 * g + 1]),
-                                detail::pack_bf16x2(f[8 * g + 2], f[8 * g + 3]),
-                                detail::pack_bf16x2(f[8 * g + 4], f[8 * g + 5]),
-                                detail::pack_bf16x2(f[8 * g + 6], f[8 * g + 7]));
-            if (h == 1 || gj + 32 >= cols) {
-              ptx::fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                ptx::tma_store_3d(&P.tmOut, stg, gj - h * 32, row_w, 0);
-                ptx::bulk_commit();
+              for (int k = 0; k < 16; ++k) w[k] = detail::pack_bf16x2(f[2 * k], f[2 * k + 1]);
+              bf16* to = static_cast<bf16*>(P.out) + static_cast<long long>(row) * P.ld + gj;
+              if (P.sectors && gj + 32 <= cols) {
+                store_sector(to, w);
+                store_sector(to + 16, w + 8);
+              } else {
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                  if (gj + 8 * g < cols) ptx::st_global_v4(to + 8 * g, w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
               }
             }
           } else {
@@ -424,15 +484,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
           }
         }
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        // The pair's next MMAs write both CTAs' accumulators.
-        if (leader)
-          ptx::mbar_arrive(tempty(buf));
-        else
-          ptx::mbar_arrive_remote(ptx::mapa(tempty(buf), 0));
-      }
+      if (col0 >= cols) release();  // nothing to read
       if (MODE == kLogits && P.stat != nullptr && live && col0 < cols)
         P.stat[static_cast<long long>(row) * P.stat_ld + P.stat0 + col0 / kHeadHalf] =
             make_float2(mx, (s4[0] + s4[1]) + (s4[2] + s4[3]));
