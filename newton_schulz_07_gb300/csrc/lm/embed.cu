@@ -73,10 +73,12 @@ constexpr int kMaxDigit = 9;            // bits a pass sorts by
 constexpr int kBins = 1 << kMaxDigit;
 constexpr int kSortWarps = 32;
 constexpr int kSortUnroll = 8;          // elements a thread loads at once
-// CTAs of the sort: 8, or 4 where the launch also zeroes rows, since clusters
-// of 8 leave a sixth of the SMs without a CTA (clusters of 4 a twentieth) and
-// the zeroing takes longer than the sort.
+// CTAs of the sort: 8, or 4 where the launch zeroes so much that this takes
+// longer than the sort: clusters of 8 leave a sixth of the SMs without a CTA,
+// clusters of 4 a twentieth (65536 tokens, 131072 rows: 8 KB a row 318 us with
+// 8, 251 with 4; 32 bytes a row 64 and 98 us).
 constexpr int kSortAlone = 8, kSortBeside = 4;
+constexpr long long kMuchZeroing = 400LL << 20;  // bytes of the table, about 60 us
 constexpr size_t kSortSmem = sizeof(int) * kSortWarps * kBins;
 constexpr unsigned int kZeroWindow = 1 << 17;  // rows whose presence a zeroing CTA holds at once
 static_assert(kZeroWindow / 8 <= kRankSmem && kZeroWindow / 8 <= kSortSmem, "presence bits");
@@ -232,12 +234,16 @@ __global__ void __launch_bounds__(32 * kSortWarps)
     ptx::cluster_sync();
     int before_cta = 0, all = 0;
     if (tid < bins) {
+      int c[ctas];
+#pragma unroll
       for (int r = 0; r < ctas; ++r) {
-        int c;
-        const uint32_t a = ptx::mapa(ptx::smem_u32(&totals[tid]), static_cast<uint32_t>(r));
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(a) : "memory");
-        if (r < rank) before_cta += c;
-        all += c;
+        const uint32_t from = ptx::mapa(ptx::smem_u32(&totals[tid]), static_cast<uint32_t>(r));
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c[r]) : "r"(from));
+      }
+#pragma unroll
+      for (int r = 0; r < ctas; ++r) {
+        if (r < rank) before_cta += c[r];
+        all += c[r];
       }
     }
     // Exclusive scan of the digits' totals.
@@ -604,20 +610,19 @@ cudaError_t launch_sort(const SortBy& by, const ZeroRows& zero, uint8_t* ws, con
   int passes, digit;
   sort_plan(none_of(by), &passes, &digit);
   unsigned long long *even = (passes & 1) ? last : other, *odd = (passes & 1) ? other : last;
-  static std::atomic<unsigned long long> configured[2];
-  if (zero.table == nullptr) {
-    const cudaError_t e = allow_smem(token_sort<kSortAlone>, static_cast<int>(kSortSmem), &configured[0]);
+  const auto launch = [&](auto kernel, int ctas, std::atomic<unsigned long long>* configured) {
+    const cudaError_t e = allow_smem(kernel, static_cast<int>(kSortSmem), configured);
     if (e != cudaSuccess) return e;
-    return mns::launch_pdl_cluster(token_sort<kSortAlone>, dim3(kSortAlone), dim3(32 * kSortWarps), kSortSmem, stream,
-                                   kSortAlone, by, zero, passes, digit, even, odd);
-  }
-  const cudaError_t e = allow_smem(token_sort<kSortBeside>, static_cast<int>(kSortSmem), &configured[1]);
-  if (e != cudaSuccess) return e;
-  // One CTA fits an SM; a twentieth of the SMs stays without a cluster.
-  const int clusters = sms * 19 / 20 / kSortBeside;
-  return mns::launch_pdl_cluster(token_sort<kSortBeside>, dim3(kSortBeside * (clusters < 2 ? 2 : clusters)),
-                                 dim3(32 * kSortWarps), kSortSmem, stream, kSortBeside, by, zero, passes, digit, even,
-                                 odd);
+    // One CTA fits an SM, and not every SM a cluster.
+    int clusters = zero.table == nullptr ? 1 : (ctas == kSortBeside ? sms * 19 / 20 : sms * 5 / 6) / ctas;
+    if (zero.table != nullptr && clusters < 2) clusters = 2;
+    return mns::launch_pdl_cluster(kernel, dim3(clusters * ctas), dim3(32 * kSortWarps), kSortSmem, stream, ctas, by,
+                                   zero, passes, digit, even, odd);
+  };
+  static std::atomic<unsigned long long> configured[2];
+  if (zero.table != nullptr && by.vocab * zero.row_bytes > kMuchZeroing)
+    return launch(token_sort<kSortBeside>, kSortBeside, &configured[0]);
+  return launch(token_sort<kSortAlone>, kSortAlone, &configured[1]);
 }
 
 cudaError_t launch_row_sums(const void* src, int src_type, long long tokens, long long vocab, int dim, float scale,

@@ -46,7 +46,9 @@ namespace {
 
 constexpr float kTopSum = 1.8446744e19f;  // 2^64
 constexpr int kHeadPairs = 76;            // CTA pairs the splits are chosen for
-constexpr int kHeadGroup = 8;             // pair rows walked together
+// Pair rows walked together: of e or W as many are read again as there are
+// bands.  (8 to 32 for the logits differ by half a percent at 8192 tokens.)
+constexpr int kHeadGroup = 8, kLogitsGroup = 16;
 constexpr long long kPieceBytes = 1LL << 32;  // e of one piece, at most, by default
 
 constexpr int kSplitTiles = 16 * kHeadPairs;  // tiles of all splits of dh, at most
@@ -492,6 +494,7 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
   auto logits = [&](long long j, bool stats, bool store, const int* redo) -> int {
     HeadGemm P = G;
     P.vp = static_cast<int>(width(j));
+    P.group = kLogitsGroup;
     P.ref = R.ref;
     P.stat = stats ? reinterpret_cast<float2*>(at(L.stat)) : nullptr;
     P.stat_ld = L.halves;
