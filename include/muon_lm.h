@@ -46,14 +46,15 @@ enum { MUON_LM_BF16 = 0, MUON_LM_F32 = 1 };
 int muon_embed(const void* table, int table_type, long long vocab, int dim, const void* ids, int ids_bits,
                long long tokens, float scale, void* out, int out_type, cudaStream_t stream);
 
+/* 0 up to 512 tokens: the workspace may then be NULL. */
 int muon_embed_grad_workspace_size(long long tokens, long long vocab, int dim, size_t* bytes);
 
 /* dtable[v] = scale * sum over the tokens t with ids[t] == v of dy[t]
  * (accumulate != 0: added to dtable[v], rows without tokens left alone; else
  * every row is written, zero where no token names it).
  *   dy  [tokens][dim], dtable  [vocab][dim]; no overlap.
- * The tokens are sorted by id (stable), and each row is summed in fp32 in
- * token order, long rows in fixed pieces that are then joined in order. */
+ * More than 512 tokens are sorted by id (stable).  Each row is summed in fp32
+ * in token order, long rows in fixed pieces that are then joined in order. */
 int muon_embed_grad(const void* dy, int dy_type, const void* ids, int ids_bits, long long tokens, long long vocab,
                     int dim, float scale, void* dtable, int dtable_type, int accumulate, void* workspace,
                     size_t workspace_bytes, cudaStream_t stream);
@@ -72,6 +73,7 @@ int muon_embed_grad(const void* dy, int dy_type, const void* ids, int ids_bits, 
 int muon_layer_norm(const void* x, int x_type, const void* weight, const void* bias, int w_type, long long rows,
                     int dim, float eps, void* y, float* mean, float* rstd, cudaStream_t stream);
 
+/* 0 for few rows: the workspace may then be NULL. */
 int muon_layer_norm_grad_workspace_size(long long rows, int dim, size_t* bytes);
 
 /* Gradient, from the mean and rstd that muon_layer_norm wrote.  With

@@ -81,6 +81,7 @@ constexpr int kSortAlone = 8, kSortBeside = 4;
 constexpr long long kMuchZeroing = 400LL << 20;  // bytes of the table, about 60 us
 constexpr size_t kSortSmem = sizeof(int) * kSortWarps * kBins;
 constexpr unsigned int kZeroWindow = 1 << 17;  // rows whose presence a zeroing CTA holds at once
+constexpr unsigned int kFewWindow = 1 << 15;
 static_assert(kZeroWindow / 8 <= kRankSmem && kZeroWindow / 8 <= kSortSmem, "presence bits");
 
 template <typename V>
@@ -88,9 +89,10 @@ __device__ __forceinline__ void zero_row(uint8_t* row, long long bytes, int lane
   for (long long c = lane * sizeof(V); c < bytes; c += 32 * sizeof(V)) *reinterpret_cast<V*>(row + c) = V{};
 }
 
-// CTA `cta` of `ctas` (1024 threads): zeroes, of rows cta, cta + ctas, ..., those
+// CTA `cta` of `ctas` zeroes, of rows cta, cta + ctas, ..., those
 // that no token names, as its own reading of the ids says.  (Rows in turn, not
 // in parts: frequent ids lie together.)
+template <unsigned int kWindow>
 __device__ __forceinline__ void zero_absent(const SortBy& by, const ZeroRows& zero, int cta, int ctas, unsigned int* bits) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const unsigned int n = static_cast<unsigned int>((by.vocab - cta + ctas - 1) / ctas);  // rows of this CTA
@@ -98,12 +100,12 @@ __device__ __forceinline__ void zero_absent(const SortBy& by, const ZeroRows& ze
   uint8_t* table = static_cast<uint8_t*>(zero.table);
   const long long rb = zero.row_bytes;
   const unsigned long long step = static_cast<unsigned long long>(rb) | reinterpret_cast<uintptr_t>(table);
-  for (unsigned int a = 0; a < n; a += kZeroWindow) {
-    const unsigned int m = n - a < kZeroWindow ? n - a : kZeroWindow;
-    for (unsigned int i = tid; i < (m + 31) / 32; i += 1024) bits[i] = 0u;
+  for (unsigned int a = 0; a < n; a += kWindow) {
+    const unsigned int m = n - a < kWindow ? n - a : kWindow;
+    for (unsigned int i = tid; i < (m + 31) / 32; i += blockDim.x) bits[i] = 0u;
     __syncthreads();
 #pragma unroll 8
-    for (long long t = tid; t < by.tokens; t += 1024) {
+    for (long long t = tid; t < by.tokens; t += blockDim.x) {
       const unsigned int key = sort_key(by, t);
       // key / ctas and the remainder, from a quotient that may be a few short.
       unsigned int q = __umulhi(key, inverse), r = key - q * ctas;
@@ -118,7 +120,7 @@ __device__ __forceinline__ void zero_absent(const SortBy& by, const ZeroRows& ze
       }
     }
     __syncthreads();
-    for (unsigned int i = warp; i < m; i += 32) {
+    for (unsigned int i = warp; i < m; i += blockDim.x >> 5) {
       if ((bits[i >> 5] >> (i & 31)) & 1u) continue;
       uint8_t* row = table + (static_cast<long long>(a + i) * ctas + cta) * rb;
       if ((step & 31) == 0) {
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(1024)
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   if (static_cast<int>(blockIdx.x) >= blocks) {
-    zero_absent(by, zero, static_cast<int>(blockIdx.x) - blocks, static_cast<int>(gridDim.x) - blocks, keys);
+    zero_absent<kZeroWindow>(by, zero, static_cast<int>(blockIdx.x) - blocks, static_cast<int>(gridDim.x) - blocks, keys);
     return;
   }
   unsigned int key;
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(32 * kSortWarps)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(blockIdx.x);
   if (rank >= ctas) {
-    zero_absent(by, zero, rank - ctas, static_cast<int>(gridDim.x) - ctas, sort_smem);
+    zero_absent<kZeroWindow>(by, zero, rank - ctas, static_cast<int>(gridDim.x) - ctas, sort_smem);
     return;
   }
   int* cnt = reinterpret_cast<int*>(sort_smem);
@@ -418,6 +420,113 @@ __global__ void __launch_bounds__(32 * kSumWarps) row_sums(const SumParams P) {
   }
 }
 
+// Few tokens: a warp takes a token and 256 columns and, if no earlier token has
+// its id, adds the rows of all that do, in token order, so no sort and no
+// partial rows are needed; other CTAs zero the rows that no token names.
+constexpr int kFewTokens = 512;
+
+template <typename TS, typename TO, int VEC>
+__global__ void __launch_bounds__(32 * kSumWarps)
+    row_sums_few(const SortBy by, const ZeroRows zero, int blocks, const SumParams P) {
+  constexpr int kK = 8 / VEC;
+  __shared__ unsigned int bits[kFewWindow / 32];
+  __shared__ unsigned int keys[kFewTokens];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  if (static_cast<int>(blockIdx.x) >= blocks) {
+    zero_absent<kFewWindow>(by, zero, static_cast<int>(blockIdx.x) - blocks, static_cast<int>(gridDim.x) - blocks, bits);
+    return;
+  }
+  const int n = static_cast<int>(by.tokens);
+  const unsigned int none = static_cast<unsigned int>(none_of(by));
+  for (int t = threadIdx.x; t < (n + 31) / 32 * 32; t += 32 * kSumWarps) keys[t] = t < n ? sort_key(by, t) : none;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  const long long item = static_cast<long long>(blockIdx.x) * kSumWarps + (threadIdx.x >> 5);
+  if (item >= static_cast<long long>(n) * P.slices) return;
+  const int t0 = static_cast<int>(item / P.slices), s = static_cast<int>(item - static_cast<long long>(t0) * P.slices);
+  const unsigned int key = keys[t0];
+  if (key == none) return;
+  for (int b = 0; b < t0; b += 32)
+    if (__any_sync(0xFFFFFFFFu, b + lane < t0 && keys[b + lane] == key)) return;
+  const TS* src = static_cast<const TS*>(P.src);
+  float a[kK][VEC] = {};
+  for (int b = t0 & ~31; b < n; b += 32) {
+    unsigned int same = __ballot_sync(0xFFFFFFFFu, b + lane >= t0 && keys[b + lane] == key);
+    while (same != 0u) {
+      Vec<TS, VEC> v[kSumUnroll][kK];
+      unsigned int m = same;
+#pragma unroll
+      for (int u = 0; u < kSumUnroll; ++u) {
+        if (m != 0u) {
+          const long long t = b + __ffs(m) - 1;
+          m &= m - 1u;
+#pragma unroll
+          for (int k = 0; k < kK; ++k) {
+            const int c = slice_col<VEC>(s, lane, k);
+            if (c < P.dim) v[u][k] = load_global<TS, VEC>(src + t * P.dim + c);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kSumUnroll; ++u) {
+        if (same != 0u) {
+          same &= same - 1u;
+#pragma unroll
+          for (int k = 0; k < kK; ++k)
+            if (slice_col<VEC>(s, lane, k) < P.dim)
+#pragma unroll
+              for (int j = 0; j < VEC; ++j) a[k][j] += to_f32(v[u][k].v[j]);
+        }
+      }
+    }
+  }
+  write_row<TO, VEC>(static_cast<TO*>(P.out) + static_cast<long long>(key) * P.dim, s, lane, P.dim, P.scale,
+                     P.accumulate, a);
+}
+
+// Few sorted tokens into compact rows: a warp takes a sorted position and 256
+// columns and, if a row begins there, adds all of it.
+template <int VEC>
+__global__ void __launch_bounds__(32 * kSumWarps) row_sums_runs(const SumParams P) {
+  static_assert(VEC == 8, "the head's rows");
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const long long item = static_cast<long long>(blockIdx.x) * kSumWarps + (threadIdx.x >> 5);
+  if (item >= P.tokens * P.slices) return;
+  const int p0 = static_cast<int>(item / P.slices), s = static_cast<int>(item - static_cast<long long>(p0) * P.slices);
+  const int n = static_cast<int>(P.tokens);
+  const unsigned int key = key_of(P.sorted[p0]);
+  if (key == static_cast<unsigned int>(P.vocab) || (p0 > 0 && key_of(P.sorted[p0 - 1]) == key)) return;
+  if (s == 0 && lane == 0) P.slot[key] = p0;
+  const int c = slice_col<VEC>(s, lane, 0);
+  const bf16* src = static_cast<const bf16*>(P.src);
+  float a[1][VEC] = {};
+  for (int b = p0; b < n; b += 32) {
+    const unsigned long long e = b + lane < n ? P.sorted[b + lane] : ~0ull;
+    const float coef = b + lane < n ? P.coef[b + lane] : 0.0f;
+    const int m = __popc(__ballot_sync(0xFFFFFFFFu, key_of(e) == key));  // contiguous from b
+    for (int q = 0; q < m; q += kSumUnroll) {
+      Vec<bf16, VEC> v[kSumUnroll];
+#pragma unroll
+      for (int u = 0; u < kSumUnroll; ++u) {
+        const long long t = __shfl_sync(0xFFFFFFFFu, token_of(e), (q + u) & 31);
+        if (q + u < m && c < P.dim) v[u] = load_global<bf16, VEC>(src + t * P.dim + c);
+      }
+#pragma unroll
+      for (int u = 0; u < kSumUnroll; ++u) {
+        const float f = __shfl_sync(0xFFFFFFFFu, coef, (q + u) & 31);
+        if (q + u < m && c < P.dim)
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) a[0][j] = fmaf(f, to_f32(v[u].v[j]), a[0][j]);
+      }
+    }
+    if (m < 32) break;
+  }
+  write_row<float, VEC>(static_cast<float*>(P.out) + static_cast<long long>(p0) * P.dim, s, lane, P.dim, 1.0f, 0, a);
+}
+
 constexpr int kShortRun = 12;  // pieces of a row that one warp joins
 
 // Sum over pieces [b, e) of a row's partial rows, `first` being the piece it
@@ -640,11 +749,33 @@ cudaError_t launch_row_sums(const void* src, int src_type, long long tokens, lon
   });
 }
 
+// Both for few tokens, in one launch.
+cudaError_t launch_few(const SortBy& by, const ZeroRows& zero, const void* src, int src_type, int dim, float scale,
+                       void* out, int out_type, int accumulate, cudaStream_t stream) {
+  SumLayout L = {};
+  const SumParams P = sum_params(src, by.tokens, by.vocab, dim, scale, out, accumulate, nullptr, L);
+  const int vec = min_vec(vec_of(dim, src, src_type), vec_of(dim, out, out_type));
+  const int blocks = static_cast<int>((by.tokens * P.slices + kSumWarps - 1) / kSumWarps);
+  const int most = 8 * sm_count();
+  const int zeros = zero.table == nullptr ? 0 : static_cast<int>(by.vocab < most ? by.vocab : most);
+  return with_type(src_type, [&](auto st) {
+    return with_type(out_type, [&](auto ot) {
+      return with_vec(vec, [&](auto vc) {
+        return mns::launch_pdl(row_sums_few<decltype(st), decltype(ot), decltype(vc)::value>, dim3(blocks + zeros),
+                               dim3(32 * kSumWarps), 0, stream, by, zero, blocks, P);
+      });
+    });
+  });
+}
+
 cudaError_t launch_row_sums_compact(const void* src, const float* coef, long long tokens, long long vocab, int dim,
                                     float* out, int* slot, uint8_t* ws, const SumLayout& L, cudaStream_t stream) {
   SumParams P = sum_params(src, tokens, vocab, dim, 1.0f, out, 0, ws, L);
   P.coef = coef;
   P.slot = slot;
+  if (tokens <= kFewTokens)
+    return mns::launch_pdl(row_sums_runs<8>, dim3(static_cast<unsigned>((tokens * P.slices + kSumWarps - 1) / kSumWarps)),
+                           dim3(32 * kSumWarps), 0, stream, P);
   return launch_sums<bf16, float, 8, true>(P, stream);  // the head's rows are multiples of 8
 }
 
@@ -690,7 +821,7 @@ int muon_embed_grad_workspace_size(long long tokens, long long vocab, int dim, s
   const int s = check(tokens, vocab, dim, 32);
   if (s != MUON_NS_OK) return s;
   if (!bytes) return MUON_NS_ERR_INVALID_ARG;
-  *bytes = tokens == 0 || vocab == 0 || dim == 0 ? 0 : sum_layout(tokens, dim).total;
+  *bytes = tokens <= kFewTokens || vocab == 0 || dim == 0 ? 0 : sum_layout(tokens, dim).total;
   return MUON_NS_OK;
 }
 
@@ -708,13 +839,15 @@ int muon_embed_grad(const void* dy, int dy_type, const void* ids, int ids_bits, 
   if (tokens > 0 && overlap(dy, static_cast<size_t>(tokens) * dim * type_size(dy_type), dtable, table_bytes))
     return MUON_NS_ERR_INVALID_ARG;
   const SumLayout L = sum_layout(tokens, dim);
-  if (tokens > 0 && (!workspace || workspace_bytes < L.total)) return MUON_NS_ERR_WORKSPACE;
+  if (tokens > kFewTokens && (!workspace || workspace_bytes < L.total)) return MUON_NS_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MUON_NS_ERR_ALIGNMENT;
   if ((s = muon_ns_device_supported(-1)) != MUON_NS_OK) return s;
   if (tokens == 0) return accumulate ? MUON_NS_OK : status_of(cudaMemsetAsync(dtable, 0, table_bytes, stream));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const SortBy by = {ids, ids_bits == 64 ? 1 : 0, tokens, vocab, -1, 0, nullptr};
   const ZeroRows zero = {accumulate ? nullptr : dtable, static_cast<long long>(dim) * type_size(dtable_type)};
+  if (tokens <= kFewTokens)
+    return status_of(launch_few(by, zero, dy, dy_type, dim, scale, dtable, dtable_type, accumulate ? 1 : 0, stream));
   const cudaError_t e = launch_sort(by, zero, ws, L, stream);
   if (e != cudaSuccess) return status_of(e);
   return status_of(launch_row_sums(dy, dy_type, tokens, vocab, dim, scale, dtable, dtable_type, accumulate ? 1 : 0, ws,

@@ -23,37 +23,61 @@ constexpr int kRingPer = 32;  // with x and dy in shared memory (dw and db)
 constexpr int kBwdMax = 1024 * kBwdPer;
 constexpr int kRingMax = 512 * kRingPer;
 constexpr int kRingSmem = 200 * 1024;
+constexpr int kFewCta = 512;  // CTA size for few rows
+constexpr int kFewSmem = sizeof(float) * 2 * kFewCta * kBwdPer;
 
 // part: fp32 [gridDim.x][2][dim], this CTA's dw and db.
-template <typename T, typename TW, int VEC, int G>
-__global__ void __launch_bounds__(G > kNormCta ? G : kNormCta)
+// FEW: the grid is one cluster, whose CTAs add their sums through each other's
+// shared memory (in rank order), so few rows take one launch and no workspace.
+template <typename T, typename TW, int VEC, int G, bool FEW>
+__global__ void __launch_bounds__(FEW ? kFewCta : (G > kNormCta ? G : kNormCta))
     layer_norm_bwd(const T* dy, const T* x, const TW* __restrict__ w, const float* __restrict__ mean,
                    const float* __restrict__ rstd, long long rows, int dim, float inv_dim, T* dx,
-                   float* __restrict__ part) {
-  constexpr int kRows = (G > kNormCta ? G : kNormCta) / G;
+                   float* __restrict__ part, float* __restrict__ dweight, float* __restrict__ dbias) {
+  constexpr int kRows = (FEW ? kFewCta : (G > kNormCta ? G : kNormCta)) / G;
   constexpr int kK = kBwdPer / VEC;
   __shared__ float red[2][2][32];
-  extern __shared__ float acc[];  // [kRows][2][dim], only with kRows > 1
+  extern __shared__ float acc[];  // [kRows][2][dim], only with kRows > 1 or FEW
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int tid = threadIdx.x & (G - 1), grp = threadIdx.x / G;
   float dw[kK][VEC] = {}, db[kK][VEC] = {};
   const long long stride = static_cast<long long>(gridDim.x) * kRows;
   int buf = 0;
-  // Every group of the CTA makes the same number of turns (barriers inside).
-  for (long long r0 = static_cast<long long>(blockIdx.x) * kRows; r0 < rows; r0 += stride, buf ^= 1) {
-    const long long row = r0 + grp;
-    const bool live = row < rows;
-    Vec<T, VEC> xv[kK], gv[kK];
+  Vec<T, VEC> xv[kK], gv[kK], xn[FEW ? kK : 1], gn[FEW ? kK : 1];
+  float mu = 0.0f, r = 0.0f, mu_next = 0.0f, r_next = 0.0f;
+  auto fetch = [&](long long row, auto& xs, auto& gs, float& m, float& q) {
+    if (row >= rows) return;
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
       const int c = (k * G + tid) * VEC;
-      if (live && c < dim) {
-        xv[k] = load_global<T, VEC>(x + row * dim + c);
-        gv[k] = load_global<T, VEC>(dy + row * dim + c);
+      if (c < dim) {
+        xs[k] = load_global<T, VEC>(x + row * dim + c);
+        gs[k] = load_global<T, VEC>(dy + row * dim + c);
       }
     }
-    const float mu = live ? mean[row] : 0.0f, r = live ? rstd[row] : 0.0f;
+    m = mean[row];
+    q = rstd[row];
+  };
+  const long long first = static_cast<long long>(blockIdx.x) * kRows;
+  if constexpr (FEW) fetch(first + grp, xn, gn, mu_next, r_next);
+  // Every group of the CTA makes the same number of turns (barriers inside).
+  for (long long r0 = first; r0 < rows; r0 += stride, buf ^= 1) {
+    const long long row = r0 + grp;
+    const bool live = row < rows;
+    if constexpr (FEW) {
+      // One row ahead: a CTA an SM leaves nothing else to hide the loads.
+#pragma unroll
+      for (int k = 0; k < kK; ++k) {
+        xv[k] = xn[k];
+        gv[k] = gn[k];
+      }
+      mu = mu_next;
+      r = r_next;
+      fetch(row + stride, xn, gn, mu_next, r_next);
+    } else {
+      fetch(row, xv, gv, mu, r);
+    }
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
@@ -89,8 +113,8 @@ __global__ void __launch_bounds__(G > kNormCta ? G : kNormCta)
       }
     }
   }
-  float* mine = part + static_cast<long long>(blockIdx.x) * 2 * dim;
-  if (kRows > 1) {
+  float* mine = FEW ? acc : part + static_cast<long long>(blockIdx.x) * 2 * dim;
+  if (kRows > 1 || FEW) {
     // The groups hold the same columns: added in group order.
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
@@ -122,6 +146,29 @@ __global__ void __launch_bounds__(G > kNormCta ? G : kNormCta)
         }
       }
     }
+  }
+  if (FEW) {
+    const int ctas = static_cast<int>(gridDim.x);
+    __syncthreads();
+    if (ctas > 1) ptx::cluster_sync();
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < 2 * dim; i += ctas * blockDim.x) {
+      float s = 0.0f;
+      for (int r = 0; r < ctas; ++r) {
+        float v;
+        if (ctas > 1)
+          asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                       : "=f"(v)
+                       : "r"(ptx::mapa(ptx::smem_u32(&acc[i]), static_cast<uint32_t>(r))));
+        else
+          v = acc[i];
+        s += v;
+      }
+      if (i < dim)
+        dweight[i] = s;
+      else if (dbias != nullptr)
+        dbias[i - dim] = s;
+    }
+    if (ctas > 1) ptx::cluster_sync();  // no CTA leaves while another reads its sums
   }
 }
 
@@ -337,6 +384,17 @@ bool use_ring(int dim, int x_type, int vec) {
   return dim <= kRingMax && vec * type_size(x_type) >= 4 && ring_smem(dim, x_type) <= kRingSmem;
 }
 
+// CTAs of the one cluster that few rows take (1, 2, 4 or 8), or 0.  Up to 9
+// turns of it: a turn is about 1.3 us, the second launch and the workspace it
+// saves about 4 on the device and 5 to issue.
+int few_ctas(long long rows, int dim) {
+  const int g = group_of(dim, kBwdPer);
+  if (g > kFewCta || rows > 9LL * 8 * (kFewCta / g)) return 0;
+  int n = 1;
+  while (n < 8 && n * (kFewCta / g) < rows) n *= 2;
+  return n;
+}
+
 // Partial rows of dw and db: CTAs of the backward kernel.  Two CTAs of 256
 // threads an SM, or one of more threads, but no more than there are rows.
 int bwd_parts(long long rows, int dim, int per_thread) {
@@ -375,7 +433,8 @@ int muon_layer_norm_grad_workspace_size(long long rows, int dim, size_t* bytes) 
   if (s != MUON_NS_OK) return s;
   if (!bytes) return MUON_NS_ERR_INVALID_ARG;
   // The type and the alignment of the call's rows choose between the kernels.
-  const int a = rows == 0 ? 0 : bwd_parts(rows, dim, kBwdPer), b = rows == 0 ? 0 : bwd_parts(rows, dim, kRingPer);
+  const bool none = rows == 0 || few_ctas(rows, dim) > 0;
+  const int a = none ? 0 : bwd_parts(rows, dim, kBwdPer), b = none ? 0 : bwd_parts(rows, dim, kRingPer);
   *bytes = align_up(sizeof(float) * 2 * static_cast<size_t>(a > b ? a : b) * dim, 256);
   return MUON_NS_OK;
 }
@@ -396,7 +455,7 @@ int muon_layer_norm_grad(const void* dy, const void* x, int x_type, const void* 
     return MUON_NS_ERR_ALIGNMENT;
   size_t need = 0;
   muon_layer_norm_grad_workspace_size(rows, dim, &need);
-  if (rows > 0 && (!workspace || workspace_bytes < need)) return MUON_NS_ERR_WORKSPACE;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MUON_NS_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MUON_NS_ERR_ALIGNMENT;
   if ((s = muon_ns_device_supported(-1)) != MUON_NS_OK) return s;
   if (rows == 0) {  // sums over no rows
@@ -408,7 +467,8 @@ int muon_layer_norm_grad(const void* dy, const void* x, int x_type, const void* 
   float* part = static_cast<float*>(workspace);
   const int vec = min_vec(min_vec(norm_vec(dim, x, x_type), norm_vec(dim, dy, x_type)),
                           min_vec(norm_vec(dim, dx, x_type), vec_of(dim, weight, w_type)));
-  const bool ring = use_ring(dim, x_type, vec);
+  const int few = few_ctas(rows, dim);
+  const bool ring = few == 0 && use_ring(dim, x_type, vec);
   const int parts = bwd_parts(rows, dim, ring ? kRingPer : kBwdPer);
   s = with_type(x_type, [&](auto xt) {
     return with_type(w_type, [&](auto wt) {
@@ -448,13 +508,24 @@ int muon_layer_norm_grad(const void* dy, const void* x, int x_type, const void* 
           constexpr int V = decltype(vc)::value, G = decltype(gc)::value;
           constexpr int T1 = G > kNormCta ? G : kNormCta;
           const size_t smem = T1 > G ? sizeof(float) * 2 * (T1 / G) * dim : 0;
-          return status_of(mns::launch_pdl(layer_norm_bwd<T, TW, V, G>, dim3(parts), dim3(T1), smem, stream, gp, xp,
-                                           wp, mean, rstd, rows, dim, inv, op, part));
+          if constexpr (G <= kFewCta) {
+            if (few > 0) {
+              auto kernel = layer_norm_bwd<T, TW, V, G, true>;
+              static std::atomic<unsigned long long> configured{0};
+              const cudaError_t e = allow_smem(kernel, kFewSmem, &configured);
+              if (e != cudaSuccess) return status_of(e);
+              return status_of(mns::launch_pdl_cluster(kernel, dim3(few), dim3(kFewCta),
+                                                       sizeof(float) * 2 * (kFewCta / G) * dim, stream, few, gp, xp, wp,
+                                                       mean, rstd, rows, dim, inv, op, part, dweight, dbias));
+            }
+          }
+          return status_of(mns::launch_pdl(layer_norm_bwd<T, TW, V, G, false>, dim3(parts), dim3(T1), smem, stream, gp, xp, wp, mean, rstd, rows, dim, inv, op, part,
+                                           dweight, dbias));
         });
       });
     });
   });
-  if (s != MUON_NS_OK) return s;
+  if (s != MUON_NS_OK || few > 0) return s;
   return status_of(mns::launch_pdl(layer_norm_join, dim3(static_cast<unsigned>((2 * dim + 31) / 32)), dim3(kNormCta), 0,
                                    stream, static_cast<const float*>(part), parts, dim, dweight, dbias));
 }

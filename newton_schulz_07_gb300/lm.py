@@ -74,6 +74,8 @@ def _workspace(workspace, device, name, *args):
     """(pointer, bytes, tensor to keep) of the caller's workspace or a new one."""
     if workspace is None:
         n = _size(name, *args)
+        if n == 0:
+            return None, 0, None
         workspace = torch.empty(n, dtype=torch.uint8, device=device)
         return workspace.data_ptr(), n, workspace
     if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.get_device() != device:

@@ -72,7 +72,7 @@ def _check(got, want, bound, names=("loss", "dh", "dW")):
 
 SHAPES = [(1, 1, 8), (1, 2, 8), (2, 7, 16), (24, 1000, 64), (63, 255, 72), (64, 256, 64), (65, 257, 136),
           (127, 1003, 264), (128, 512, 128), (129, 5003, 192), (255, 300, 1000), (257, 513, 328), (300, 2050, 512),
-          (700, 777, 64), (1030, 1300, 264), (40, 20011, 776)]
+          (700, 777, 64), (1030, 1300, 264), (40, 20011, 776), (512, 20, 72), (513, 20, 72), (5000, 600, 72)]
 
 
 @pytest.mark.parametrize("n,v,d", SHAPES)

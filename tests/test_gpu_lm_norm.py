@@ -15,7 +15,7 @@ E = 2.0 ** -24
 U = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -23}
 T = {"bf16": torch.bfloat16, "fp32": torch.float32}
 SHAPES = [(1, 1), (1, 8), (3, 5), (2, 31), (9, 768), (1, 1001), (33, 1024), (130, 2050), (7, 4096), (5, 4099), (301, 264),
-          (4, 8192), (3, 8200), (2, 16384), (2, 16390), (2, 32768), (2, 32776), (3, 40001)]
+          (4, 8192), (3, 8200), (2, 16384), (2, 16390), (2, 32768), (2, 32776), (3, 40001), (384, 300), (385, 300), (48, 4096), (49, 4096)]
 
 
 def _values(shape, seed, dtype, scale=1.0, shift=0.0):

@@ -15,6 +15,7 @@ def _c(*shape, dtype=torch.float32):
 def test_embedding():
     table, ids = _c(10, 8), _c(4, dtype=torch.int64)
     dy = _c(4, 8)
+    many, mdy = _c(600, dtype=torch.int64), _c(600, 8)
     for error, f in (
             (TypeError, lambda: ns.muon_embed(table.half(), ids)), (TypeError, lambda: ns.muon_embed(table, ids.short())),
             (TypeError, lambda: ns.muon_embed(table, ids.cpu())), (ValueError, lambda: ns.muon_embed(table[0], ids)),
@@ -27,13 +28,14 @@ def test_embedding():
             (ValueError, lambda: ns.muon_embed_grad(dy, ids, 10, accumulate=True)),
             (ValueError, lambda: ns.muon_embed_grad(dy, ids, 10, dtable=_c(9, 8))),
             (ValueError, lambda: ns.muon_embed_grad(dy, ids, 10, workspace=torch.zeros(1 << 16, dtype=torch.uint8))),
-            (ns.MuonNSError, lambda: ns.muon_embed_grad(dy, ids, 10, workspace=_c(8)))):
+            (ns.MuonNSError, lambda: ns.muon_embed_grad(mdy, many, 10, workspace=_c(8)))):
         with pytest.raises(error):
             f()
 
 
 def test_layer_norm():
     x, w, m = _c(4, 8), _c(8), _c(4)
+    big, bm = _c(30000, 8), _c(30000)
     for error, f in (
             (TypeError, lambda: ns.muon_layer_norm(x.half(), w)), (ValueError, lambda: ns.muon_layer_norm(x, w[:7])),
             (TypeError, lambda: ns.muon_layer_norm(x, w, w.bfloat16())), (ValueError, lambda: ns.muon_layer_norm(x.t(), _c(4))),
@@ -42,6 +44,6 @@ def test_layer_norm():
             (TypeError, lambda: ns.muon_layer_norm_grad(x.bfloat16(), x, w, m, m)),
             (ValueError, lambda: ns.muon_layer_norm_grad(x[:3], x, w, m, m)), (ValueError, lambda: ns.muon_layer_norm_grad(x, x, w, m[:3], m)),
             (TypeError, lambda: ns.muon_layer_norm_grad(x, x, w, m.bfloat16(), m)),
-            (ns.MuonNSError, lambda: ns.muon_layer_norm_grad(x, x, w, m, m, workspace=_c(1)))):
+            (ns.MuonNSError, lambda: ns.muon_layer_norm_grad(big, big, w, bm, bm, workspace=_c(1)))):
         with pytest.raises(error):
             f()

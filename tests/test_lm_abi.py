@@ -63,7 +63,7 @@ def test_embed_refusals(kw, code):
 
 
 def _embed_grad(**kw):
-    a = dict(dy=1 << 20, dt=0, ids=P, bits=32, tokens=4, vocab=10, dim=8, scale=1.0, out=1 << 21, ot=1, acc=0, ws=1 << 22,
+    a = dict(dy=1 << 20, dt=0, ids=P, bits=32, tokens=600, vocab=10, dim=8, scale=1.0, out=1 << 21, ot=1, acc=0, ws=1 << 22,
              wsb=1 << 20)
     a.update(kw)
     return _lib.lib().muon_embed_grad(a["dy"], a["dt"], a["ids"], a["bits"], a["tokens"], a["vocab"], a["dim"], a["scale"],
@@ -97,7 +97,7 @@ def test_layer_norm_refusals(kw, code):
 
 
 def _norm_grad(**kw):
-    a = dict(dy=P, x=P, xt=0, w=P, wt=1, mean=P, rstd=P, rows=3, dim=8, dx=P, dw=P, db=P, ws=P, wsb=1 << 20)
+    a = dict(dy=P, x=P, xt=0, w=P, wt=1, mean=P, rstd=P, rows=30000, dim=8, dx=P, dw=P, db=P, ws=P, wsb=1 << 20)
     a.update(kw)
     return _lib.lib().muon_layer_norm_grad(a["dy"], a["x"], a["xt"], a["w"], a["wt"], a["mean"], a["rstd"], a["rows"],
                                            a["dim"], a["dx"], a["dw"], a["db"], a["ws"], a["wsb"], None)
@@ -122,7 +122,10 @@ def test_workspace_sizes():
     assert ns.embed_grad_workspace_size(0, 10, 8) == 0 and ns.layer_norm_grad_workspace_size(0, 8) == 0
     # Sorted pairs twice, two partial rows a piece of 32 positions.
     assert ns.embed_grad_workspace_size(1000, 100, 64) >= 16 * 1000 + 32 * 2 * 64 * 4
-    assert ns.layer_norm_grad_workspace_size(1, 24) >= 2 * 24 * 4
+    assert ns.layer_norm_grad_workspace_size(50000, 24) >= 2 * 24 * 4
+    # Few tokens and few rows need none.
+    assert ns.embed_grad_workspace_size(512, 100, 64) == 0 < ns.embed_grad_workspace_size(513, 100, 64)
+    assert ns.layer_norm_grad_workspace_size(7, 4096) == 0
     with pytest.raises(ns.MuonNSError):
         ns.embed_grad_workspace_size(-1, 10, 8)
     with pytest.raises(ns.MuonNSError):
