@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kFwdPer = 32;  // elements a thread holds
 constexpr int kFwdMax = 1024 * kFwdPer;
-constexpr int kFwdRingSmem = 108 * 1024;
+constexpr int kFwdRingSmem = 110 * 1024;
 
 // Statistics and output of NR rows of each group, from the thread's units of
 // them (rows row .. row + NR - 1, those below `rows`).  Every thread of the CTA
@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(G > kNormCta ? G : kNormCta)
 template <typename T>
 constexpr int kTurnRows = sizeof(T) == 2 ? 2 : 1;
 
-// A thread copies and reads its own elements, so the copies need no barrier.
+// A thread copies and reads its own elements, so the copies need no barrier
+// (except those by words).
 template <typename T, typename TW, int VEC, int G>
 __global__ void __launch_bounds__(G > kNormCta ? G : kNormCta, G > kNormCta ? 1 : 2)
     layer_norm_fwd_ring(const T* x, const TW* __restrict__ w, const TW* __restrict__ b, long long rows, int dim,
@@ -138,15 +139,22 @@ __global__ void __launch_bounds__(G > kNormCta ? G : kNormCta, G > kNormCta ? 1 
   ptx::griddep_wait();
   const int tid = threadIdx.x & (G - 1), grp = threadIdx.x / G;
   const long long stride = static_cast<long long>(gridDim.x) * kRows;
-  T* mine = reinterpret_cast<T*>(ring) + grp * NR * dim;
+  constexpr bool kWords = kByWords<T, VEC>;
+  const int pitch = kWords ? word_pitch(dim) : dim;
+  T* mine = reinterpret_cast<T*>(ring) + grp * NR * pitch;
   auto fetch = [&](int st, long long row) {
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       if (row + i < rows) {
+        T* to = mine + (st * kRows + i) * pitch;
+        if constexpr (kWords) {
+          copy_words<G>(to, x, row + i, rows, dim, tid);
+        } else {
 #pragma unroll
-        for (int k = 0; k < C::kK; ++k) {
-          const int c = C::first(k, tid);
-          if (c < dim) C::copy(mine + (st * kRows + i) * dim, x + (row + i) * dim, c, dim);
+          for (int k = 0; k < C::kK; ++k) {
+            const int c = C::first(k, tid);
+            if (c < dim) C::copy(to, x + (row + i) * dim, c, dim);
+          }
         }
       }
     }
@@ -160,14 +168,19 @@ __global__ void __launch_bounds__(G > kNormCta ? G : kNormCta, G > kNormCta ? 1 
     const long long row = r0 + grp * NR;
     fetch(st ^ 1, row + stride);
     copy_wait<1>();
+    if (kWords) group_barrier<G>();
     Vec<T, C::kU> v[NR][C::kK];
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
+    for (int i = 0; i < NR; ++i) {
+      const T* from = mine + (st * kRows + i) * pitch + (kWords ? row_shift(x + (row + i) * dim) : 0);
 #pragma unroll
       for (int k = 0; k < C::kK; ++k) {
         const int c = C::first(k, tid);
-        if (row + i < rows && c < dim) v[i][k] = C::template load<true>(mine + (st * kRows + i) * dim, c, dim);
+        if (row + i < rows && c < dim) v[i][k] = C::template load<true>(from, c, dim);
       }
+    }
+    // The next turn's copies go to the buffer after this one's other half: all
+    // reads of it are behind the barriers of the sums.
     norm_rows<T, TW, VEC, G, NR>(v, w, b, row, rows, dim, inv_dim, eps, y, mean, rstd, red);
   }
   copy_wait<0>();
@@ -238,13 +251,14 @@ extern "C" int muon_layer_norm(const void* x, int x_type, const void* weight, co
           constexpr int V = decltype(vc)::value, G = decltype(gc)::value;
           constexpr int T1 = G > kNormCta ? G : kNormCta;
           const long long grid = (rows + T1 / G - 1) / (T1 / G);
-          if constexpr (V * sizeof(T) >= 4 && G <= 512) {
+          if constexpr (G <= 512) {
             constexpr int NR = kTurnRows<T>;
-            const size_t smem = 2 * sizeof(T) * (T1 / G * NR) * dim;
+            const size_t smem = 2 * sizeof(T) * (T1 / G * NR) * (kByWords<T, V> ? word_pitch(dim) : dim);
             // The staying grid takes over where each of its CTAs has several
             // turns.
             const long long stay = static_cast<long long>(sm_count()) * (T1 > kNormCta ? 1 : 2);
-            if (smem <= kFwdRingSmem && grid >= 3 * NR * stay) {
+            const bool words = !kByWords<T, V> || (reinterpret_cast<uintptr_t>(x) & 3) == 0;
+            if (words && smem <= kFwdRingSmem && grid >= 3 * NR * stay) {
               auto kernel = layer_norm_fwd_ring<T, TW, V, G>;
               static std::atomic<unsigned long long> configured{0};
               const cudaError_t e = allow_smem(kernel, kFwdRingSmem, &configured);

@@ -89,6 +89,39 @@ struct Cols {
   }
 };
 
+// Rows of bf16 with an odd number of columns start on 2 bytes, less than
+// cp.async can copy.  They are copied as the 4-byte words that cover them, by a
+// group of G threads, to a buffer of word_pitch(dim) elements; the row then
+// starts at element `row_shift` of it.  A word may hold an element of the row
+// before or after; only the tensor's very last may lack its second half.
+template <typename T, int VEC>
+constexpr bool kByWords = VEC * sizeof(T) < 4;
+MNS_HD int word_pitch(int dim) { return (dim + 3) & ~1; }
+template <typename T>
+__device__ __forceinline__ int row_shift(const T* row) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 1u);
+}
+template <int G, typename T>
+__device__ __forceinline__ void copy_words(T* dst, const T* base, long long row, long long rows, int dim, int tid) {
+  const T* src = base + row * dim;
+  const int shift = row_shift(src);
+  const bool last = row == rows - 1;
+  for (int i = 2 * tid; i < dim + shift; i += 2 * G) {
+    if (last && i + 1 - shift >= dim)
+      dst[i] = src[i - shift];
+    else
+      copy_async<4>(dst + i, src + i - shift);
+  }
+}
+// Makes a group's copies (after its wait) visible to it, and its reads done.
+template <int G>
+__device__ __forceinline__ void group_barrier() {
+  if (G > 32)
+    __syncthreads();
+  else
+    __syncwarp();
+}
+
 // Threads a row takes with `per` elements each: 8 to 1024.
 inline int group_of(int dim, int per) {
   int g = 8;

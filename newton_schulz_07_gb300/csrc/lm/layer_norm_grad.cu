@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(FEW ? kFewCta : (G > kNormCta ? G : kNormCta))
 }
 
 // The same with the rows of x and dy copied to shared memory one turn ahead
-// (cp.async, a thread copies and reads its own elements, so no barrier is
-// needed for them) and read from there twice, which leaves the registers to
+// (cp.async; a thread copies and reads its own elements, so no barrier is
+// needed for them, except for those copied by words) and read from there twice, which leaves the registers to
 // kRingPer columns of dw and db a thread.
 template <typename T, typename TW, int VEC, int G>
 __global__ void __launch_bounds__(G > kNormCta ? G : kNormCta, G > kNormCta ? 1 : 2)
@@ -190,17 +190,24 @@ __global__ void __launch_bounds__(G > kNormCta ? G : kNormCta, G > kNormCta ? 1 
   ptx::griddep_wait();
   const int tid = threadIdx.x & (G - 1), grp = threadIdx.x / G;
   const long long stride = static_cast<long long>(gridDim.x) * kRows;
-  T* mine_x = reinterpret_cast<T*>(ring) + grp * dim;
-  const int turn = 2 * kRows * dim, to_dy = kRows * dim;
+  constexpr bool kWords = kByWords<T, VEC>;
+  const int pitch = kWords ? word_pitch(dim) : dim;
+  T* mine_x = reinterpret_cast<T*>(ring) + grp * pitch;
+  const int turn = 2 * kRows * pitch, to_dy = kRows * pitch;
   float mu_next = 0.0f, r_next = 0.0f;
   auto fetch = [&](int st, long long row) {
     if (row < rows) {
+      if constexpr (kWords) {
+        copy_words<G>(mine_x + st * turn, x, row, rows, dim, tid);
+        copy_words<G>(mine_x + st * turn + to_dy, dy, row, rows, dim, tid);
+      } else {
 #pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        const int c = C::first(k, tid);
-        if (c < dim) {
-          C::copy(mine_x + st * turn, x + row * dim, c, dim);
-          C::copy(mine_x + st * turn + to_dy, dy + row * dim, c, dim);
+        for (int k = 0; k < kK; ++k) {
+          const int c = C::first(k, tid);
+          if (c < dim) {
+            C::copy(mine_x + st * turn, x + row * dim, c, dim);
+            C::copy(mine_x + st * turn + to_dy, dy + row * dim, c, dim);
+          }
         }
       }
       mu_next = mean[row];
@@ -219,8 +226,9 @@ __global__ void __launch_bounds__(G > kNormCta ? G : kNormCta, G > kNormCta ? 1 
     const float mu = mu_next, r = live ? r_next : 0.0f;
     fetch(st ^ 1, row + stride);
     copy_wait<1>();
-    const T* xs = mine_x + st * turn;
-    const T* gs = xs + to_dy;
+    if (kWords) group_barrier<G>();
+    const T* xs = mine_x + st * turn + (kWords ? row_shift(x + row * dim) : 0);
+    const T* gs = mine_x + st * turn + to_dy + (kWords ? row_shift(dy + row * dim) : 0);
     // With d = x - mean and e = dy d: dw += r e, db += dy, and the row's sums
     // of dy w and e w.
     float2 s1 = both(0.0f), s2 = both(0.0f);
@@ -266,6 +274,7 @@ __global__ void __launch_bounds__(G > kNormCta ? G : kNormCta, G > kNormCta ? 1 
         }
       }
     }
+    if (kWords) group_barrier<G>();  // the row has been read before its buffer is copied to
   }
   copy_wait<0>();
   float* out = part + static_cast<long long>(blockIdx.x) * 2 * dim;
@@ -376,12 +385,13 @@ __global__ void __launch_bounds__(kNormCta)
 // also hold [rows][2][dim] fp32 at the end.
 size_t ring_smem(int dim, int x_type) {
   const int g = group_of(dim, kRingPer);
-  return static_cast<size_t>(4) * (g > kNormCta ? 1 : kNormCta / g) * dim * type_size(x_type);
+  return static_cast<size_t>(4) * (g > kNormCta ? 1 : kNormCta / g) * word_pitch(dim) * type_size(x_type);
 }
 
-// The ring needs copies of 4 bytes at least, and its two turns have to fit.
-bool use_ring(int dim, int x_type, int vec) {
-  return dim <= kRingMax && vec * type_size(x_type) >= 4 && ring_smem(dim, x_type) <= kRingSmem;
+// The ring's two turns have to fit, and its copies are of 4 bytes at least.
+bool use_ring(int dim, int x_type, int vec, const void* x, const void* dy) {
+  const bool words = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(dy)) & 3) == 0;
+  return dim <= kRingMax && (vec * type_size(x_type) >= 4 || words) && ring_smem(dim, x_type) <= kRingSmem;
 }
 
 // CTAs of the one cluster that few rows take (1, 2, 4 or 8), or 0.  Up to 9
@@ -468,7 +478,7 @@ int muon_layer_norm_grad(const void* dy, const void* x, int x_type, const void* 
   const int vec = min_vec(min_vec(norm_vec(dim, x, x_type), norm_vec(dim, dy, x_type)),
                           min_vec(norm_vec(dim, dx, x_type), vec_of(dim, weight, w_type)));
   const int few = few_ctas(rows, dim);
-  const bool ring = few == 0 && use_ring(dim, x_type, vec);
+  const bool ring = few == 0 && use_ring(dim, x_type, vec, x, dy);
   const int parts = bwd_parts(rows, dim, ring ? kRingPer : kBwdPer);
   s = with_type(x_type, [&](auto xt) {
     return with_type(w_type, [&](auto wt) {
@@ -490,7 +500,7 @@ int muon_layer_norm_grad(const void* dy, const void* x, int x_type, const void* 
         return with_norm_vec<T>(vec, [&](auto vc) {
           return with_group(group_of(dim, kRingPer), [&](auto gc) {
             constexpr int V = decltype(vc)::value, G = decltype(gc)::value;
-            if constexpr (G > 512 || V * sizeof(T) < 4) {
+            if constexpr (G > 512) {
               return static_cast<int>(MUON_NS_ERR_INVALID_ARG);  // use_ring says no
             } else {
               constexpr int T1 = G > kNormCta ? G : kNormCta;

@@ -176,6 +176,36 @@ def test_no_rows():
     assert dx.shape == (0, 24) and not dw.any() and not db.any()
 
 
+@pytest.mark.parametrize("rows,dim", [(100003, 33), (70001, 72), (40011, 264), (20011, 1001), (6001, 2050), (4001, 4099),
+                                      (2003, 8199), (1901, 16384), (5003, 6020)])
+@pytest.mark.parametrize("types", [("bf16", "fp32"), ("fp32", "bf16")])
+def test_many_rows(rows, dim, types):
+    # Rows in turns of a grid that stays; odd lengths start on any byte pair.
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x, dy = (torch.randn((rows, dim), generator=g, device="cuda").mul_(1.5).add_(s).to(T[types[0]]) for s in (0.5, 0.0))
+    w, b = (torch.randn(dim, generator=g, device="cuda").to(T[types[1]]) for _ in range(2))
+    y, mean, rstd = ns.muon_layer_norm(x, w, b)
+    dx, dw, db = ns.muon_layer_norm_grad(dy, x, w, mean, rstd)
+    S, sums, size = _terms(dim), [0, 0], [0, 0]
+    for i in range(0, rows, 4096):
+        q = slice(i, i + 4096)
+        want = _forward_bound(x[q], w, b, 1e-5)
+        for got, (ref, bound), u in zip((y[q], mean[q], rstd[q]), want, (U[x.dtype], 0, 0)):
+            assert torch.all((got.double() - ref).abs() <= bound + u * (ref.abs() + bound) + 1e-37)
+        r, gr = rstd[q].double()[:, None], dy[q].double()
+        xh = (x[q].double() - mean[q].double()[:, None]) * r
+        a = gr * w.double()
+        m1, m2 = a.mean(1, keepdim=True), (a * xh).mean(1, keepdim=True)
+        ref = r * (a - m1 - xh * m2)
+        e1, e2 = (S + 8) * E * a.abs().mean(1, keepdim=True), (S + 16) * E * (a * xh).abs().mean(1, keepdim=True)
+        bound = r * (e1 + xh.abs() * e2 + 16 * E * (a.abs() + m1.abs() + (xh * m2).abs()))
+        assert torch.all((dx[q].double() - ref).abs() <= bound + U[x.dtype] * (ref.abs() + bound) + 1e-37)
+        for k, t in enumerate((gr * xh, gr)):
+            sums[k], size[k] = sums[k] + t.sum(0), size[k] + t.abs().sum(0)
+    for got, ref, s in zip((dw, db), sums, size):
+        assert torch.all((got.double() - ref).abs() <= (rows / 64 + 128) * E * s)
+
+
 def test_many_rows_and_determinism():
     x, dy = _values((70001, 72), 21, torch.bfloat16).cuda(), _values((70001, 72), 22, torch.bfloat16).cuda()
     w = torch.ones(72, device="cuda")
