@@ -148,8 +148,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
 
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  // Read first, so that the setup below hides it.
+  const int4 ctl = *reinterpret_cast<const int4*>(P.ctl);
+  static_assert(kCtlCount == 1 && kCtlSplits == 2 && kCtlRedo == 3, "control words");
   // Nothing to do again: the whole grid leaves before it sets anything up.
-  if (MODE == kLogits && P.redo != nullptr && P.ctl[kCtlRedo] == 0) return;
+  if (MODE == kLogits && P.redo != nullptr && ctl.w == 0) return;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int crank = static_cast<int>(ptx::cluster_ctarank());
@@ -196,13 +199,13 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
 
   // The tile space: `splits` times pair rows x column tiles, split-major, so
   // that tiles running together read the same part of a split contraction.
-  const int count = P.ctl[kCtlCount];
+  const int count = ctl.y;
   const int pr = MODE >= kDwBf16 ? (P.vp + kHeadRows - 1) / kHeadRows : token_pairs(count);
   const int tn = ((MODE == kLogits ? P.vp : P.dim) + kHeadRows - 1) / kHeadRows;
   const int kb_all = MODE == kLogits ? (P.dim + kBlockK - 1) / kBlockK
                      : MODE == kDh   ? (P.vp + kBlockK - 1) / kBlockK
                                      : (count > 0 ? (count + kBlockK - 1) / kBlockK : 1);
-  const int splits = MODE == kDh ? P.ctl[kCtlSplits] : 1;
+  const int splits = MODE == kDh ? ctl.z : 1;
   // (Fewer than 2^31 tiles: the host sees to it.)
   const uint32_t tiles = static_cast<uint32_t>(pr) * static_cast<uint32_t>(tn);
   const uint32_t total = tiles * static_cast<uint32_t>(splits);
