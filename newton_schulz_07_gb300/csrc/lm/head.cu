@@ -338,7 +338,7 @@ HeadLayout head_layout(long long tokens, long long vocab, int dim, bool grad, in
   // Pieces of whole column tiles.
   long long n = grad ? pieces : 1;
   if (n <= 0) n = (2 * tokens * vocab + kPieceBytes - 1) / kPieceBytes;
-  const long long tiles = (vocab + kHeadRows - 1) / kHeadRows;
+  const long long tiles = vocab > 0 ? (vocab + kHeadRows - 1) / kHeadRows : 1;
   if (n > tiles) n = tiles;
   if (n < 1) n = 1;
   L.piece = (tiles + n - 1) / n * kHeadRows;

@@ -47,3 +47,21 @@ def test_layer_norm():
             (ns.MuonNSError, lambda: ns.muon_layer_norm_grad(big, big, w, bm, bm, workspace=_c(1)))):
         with pytest.raises(error):
             f()
+
+
+def test_head():
+    b = torch.bfloat16
+    h, w, t = _c(4, 16, dtype=b), _c(10, 16, dtype=b), _c(4, dtype=torch.int64)
+    f, g = ns.muon_head_loss, ns.muon_head_loss_grad
+    for error, call in (
+            (TypeError, lambda: f(h.float(), w, t)), (TypeError, lambda: f(h, w.float(), t)), (TypeError, lambda: f(h, w, t.float())),
+            (ValueError, lambda: f(h, w[:, :8].contiguous(), t)), (ValueError, lambda: f(h, w[0], t)), (ValueError, lambda: f(h, w, t[:3])),
+            (ValueError, lambda: f(h, _c(16, 10, dtype=b).t(), t)), (ns.MuonNSError, lambda: f(_c(4, 12, dtype=b), _c(10, 12, dtype=b), t)),
+            (ns.MuonNSError, lambda: f(h, w, t, workspace=_c(64))), (TypeError, lambda: g(h, w, t, dloss=_c(4, dtype=b))),
+            (ValueError, lambda: g(h, w, t, dloss=_c(3))), (ValueError, lambda: g(h, w, t, accumulate=True)),
+            (ValueError, lambda: g(h, w, t, dtable=_c(9, 16))), (TypeError, lambda: g(h, w, t, dtable=_c(10, 16, dtype=torch.float16))),
+            (ns.MuonNSError, lambda: g(h, w, t, dtable=_c(10, 16, dtype=b), accumulate=True)),
+            (ns.MuonNSError, lambda: g(h, w, t, dtable=w)), (ns.MuonNSError, lambda: g(h, w, t, pieces=-1)),
+            (ValueError, lambda: g(h, w, t, workspace=torch.zeros(1 << 20, dtype=torch.uint8)))):
+        with pytest.raises(error):
+            call()

@@ -112,9 +112,66 @@ def test_layer_norm_grad_refusals(kw, code):
     assert _norm_grad(**kw) == code
 
 
+H, W, T, L, DH, DW, SP = (i << 24 for i in range(1, 8))
+BIG = 1 << 40
+
+
+def _head(**kw):
+    a = dict(h=H, w=W, n=5, v=100, d=16, t=T, bits=64, ignore=-100, loss=L, ws=SP, wsb=BIG)
+    a.update(kw)
+    return _lib.lib().muon_head_loss(a["h"], a["w"], a["n"], a["v"], a["d"], a["t"], a["bits"], a["ignore"], a["loss"],
+                                     a["ws"], a["wsb"], None)
+
+
+HEAD = [(dict(n=-1), BAD), (dict(v=-1), BAD), (dict(d=0), BAD), (dict(d=-8), BAD), (dict(d=12), ALIGN),
+        (dict(n=(1 << 30) + 1), BAD), (dict(v=(1 << 30) + 1), BAD), (dict(d=(1 << 20) + 8), BAD), (dict(bits=16), BAD),
+        (dict(h=None), BAD), (dict(w=None), BAD), (dict(t=None), BAD), (dict(loss=None), BAD), (dict(h=H + 8), ALIGN),
+        (dict(w=W + 2), ALIGN), (dict(t=T + 4), ALIGN), (dict(loss=L + 2), ALIGN), (dict(ws=SP + 128), ALIGN),
+        (dict(ws=None), WS), (dict(wsb=1000), WS)]
+
+
+@pytest.mark.parametrize("kw,code", HEAD + [(dict(n=0, h=None, loss=None, ws=None), 0)])
+def test_head_loss_refusals(kw, code):
+    assert _head(**kw) == code
+
+
+def _head_grad(**kw):
+    a = dict(h=H, w=W, n=5, v=100, d=16, t=T, bits=64, ignore=-100, dloss=None, pieces=0, loss=L, dh=DH, dw=DW, dt=0, acc=0,
+             ws=SP, wsb=BIG)
+    a.update(kw)
+    return _lib.lib().muon_head_loss_grad(a["h"], a["w"], a["n"], a["v"], a["d"], a["t"], a["bits"], a["ignore"], a["dloss"],
+                                          a["pieces"], a["loss"], a["dh"], a["dw"], a["dt"], a["acc"], a["ws"], a["wsb"],
+                                          None)
+
+
+@pytest.mark.parametrize("kw,code", HEAD + [
+    (dict(pieces=-1), BAD), (dict(dt=2), BAD), (dict(acc=1), BAD), (dict(dh=None), BAD), (dict(dw=None), BAD),
+    (dict(dh=H), BAD), (dict(dh=W), BAD), (dict(dw=H), BAD), (dict(dw=W + 16), BAD), (dict(dw=DH + 32), BAD),
+    (dict(dh=DH + 8), ALIGN), (dict(dw=DW + 4), ALIGN), (dict(dloss=L + 2), ALIGN),
+    (dict(n=0, v=0, h=None, w=None, t=None, loss=None, dh=None, dw=None, ws=None), _lib.ERR_UNSUPPORTED_DEVICE
+     if not torch.cuda.is_available() else 0)])
+def test_head_loss_grad_refusals(kw, code):
+    assert _head_grad(**kw) == code
+
+
+def test_head_workspace():
+    size = ns.head_workspace_size
+    # One piece holds tokens x vocab in bf16; more pieces hold less; the losses
+    # alone hold none of it.
+    assert size(1000, 50000, 64, True, 1) >= 2 * 1000 * 50000 > size(1000, 50000, 64, True, 8) > size(1000, 50000, 64, False)
+    # By default a piece is at most about 4 GiB.
+    assert 1 << 32 <= size(200000, 131072, 64) < 6 << 30
+    assert size(0, 50000, 64) == size(1000, 0, 64) == 0
+    for bad in ((-1, 10, 8), (1, 10, 12), (1, 10, 0)):
+        with pytest.raises(ns.MuonNSError):
+            size(*bad)
+    with pytest.raises(ns.MuonNSError):
+        size(1, 10, 8, True, -1)
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device path")
 def test_valid_calls_without_a_device_are_unsupported():
-    for call in (_embed, _embed_grad, _norm, _norm_grad):
+    for call in (_embed, _embed_grad, _norm, _norm_grad, _head, _head_grad):
         assert call() == _lib.ERR_UNSUPPORTED_DEVICE
 
 
@@ -137,6 +194,8 @@ def test_workspace_sizes():
 def test_binding_refuses_host_tensors():
     x, ids = torch.ones(4, 8), torch.zeros(4, dtype=torch.int64)
     for f in (lambda: ns.muon_embed(x, ids), lambda: ns.muon_embed_grad(x, ids, 10), lambda: ns.muon_layer_norm(x, x[0]),
-              lambda: ns.muon_layer_norm_grad(x, x, x[0], x[:, 0], x[:, 0])):
+              lambda: ns.muon_layer_norm_grad(x, x, x[0], x[:, 0], x[:, 0]),
+              lambda: ns.muon_head_loss(x.bfloat16(), x.bfloat16(), ids),
+              lambda: ns.muon_head_loss_grad(x.bfloat16(), x.bfloat16(), ids)):
         with pytest.raises(TypeError):
             f()
