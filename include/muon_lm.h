@@ -46,14 +46,14 @@ enum { MUON_LM_BF16 = 0, MUON_LM_F32 = 1 };
 int muon_embed(const void* table, int table_type, long long vocab, int dim, const void* ids, int ids_bits,
                long long tokens, float scale, void* out, int out_type, cudaStream_t stream);
 
-/* 0 up to 512 tokens: the workspace may then be NULL. */
+/* 0 up to 256 tokens: the workspace may then be NULL. */
 int muon_embed_grad_workspace_size(long long tokens, long long vocab, int dim, size_t* bytes);
 
 /* dtable[v] = scale * sum over the tokens t with ids[t] == v of dy[t]
  * (accumulate != 0: added to dtable[v], rows without tokens left alone; else
  * every row is written, zero where no token names it).
  *   dy  [tokens][dim], dtable  [vocab][dim]; no overlap.
- * More than 512 tokens are sorted by id (stable).  Each row is summed in fp32
+ * More than 256 tokens are sorted by id (stable).  Each row is summed in fp32
  * in token order, long rows in fixed pieces that are then joined in order. */
 int muon_embed_grad(const void* dy, int dy_type, const void* ids, int ids_bits, long long tokens, long long vocab,
                     int dim, float scale, void* dtable, int dtable_type, int accumulate, void* workspace,

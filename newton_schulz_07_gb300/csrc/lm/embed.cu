@@ -423,7 +423,10 @@ __global__ void __launch_bounds__(32 * kSumWarps) row_sums(const SumParams P) {
 // Few tokens: a warp takes a token and 256 columns and, if no earlier token has
 // its id, adds the rows of all that do, in token order, so no sort and no
 // partial rows are needed; other CTAs zero the rows that no token names.
-constexpr int kFewTokens = 512;
+// (256 tokens into 50257 rows, added: 8 us against 13 us by sorting, 29 us where
+// nine in ten are the same; 1000 tokens 10 to 27 us, and 109 us.)
+constexpr int kFewTokens = 256;
+constexpr int kFewUnroll = 16;  // rows a warp has in flight: a frequent id's are one warp's
 
 template <typename TS, typename TO, int VEC>
 __global__ void __launch_bounds__(32 * kSumWarps)
@@ -454,10 +457,10 @@ __global__ void __launch_bounds__(32 * kSumWarps)
   for (int b = t0 & ~31; b < n; b += 32) {
     unsigned int same = __ballot_sync(0xFFFFFFFFu, b + lane >= t0 && keys[b + lane] == key);
     while (same != 0u) {
-      Vec<TS, VEC> v[kSumUnroll][kK];
+      Vec<TS, VEC> v[(sizeof(TS) == 2 ? kFewUnroll : kSumUnroll)][kK];
       unsigned int m = same;
 #pragma unroll
-      for (int u = 0; u < kSumUnroll; ++u) {
+      for (int u = 0; u < (sizeof(TS) == 2 ? kFewUnroll : kSumUnroll); ++u) {
         if (m != 0u) {
           const long long t = b + __ffs(m) - 1;
           m &= m - 1u;
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(32 * kSumWarps)
         }
       }
 #pragma unroll
-      for (int u = 0; u < kSumUnroll; ++u) {
+      for (int u = 0; u < (sizeof(TS) == 2 ? kFewUnroll : kSumUnroll); ++u) {
         if (same != 0u) {
           same &= same - 1u;
 #pragma unroll

@@ -81,7 +81,7 @@ def test_lookup_keeps_the_ids_shape_and_any_alignment():
 
 
 GRAD = [(1, 1, 1), (1, 5, 8), (2, 3, 3), (31, 7, 20), (32, 7, 64), (33, 2, 257), (64, 1, 264), (65, 1000, 40),
-        (257, 33, 1000), (512, 100, 72), (513, 100, 72), (500, 2, 9), (1000, 70000, 24), (2047, 130, 16), (2049, 130, 16), (5000, 17, 72), (20000, 3, 8),
+        (257, 33, 1000), (256, 100, 72), (512, 100, 72), (1025, 100, 72), (500, 2, 9), (1000, 70000, 24), (2047, 130, 16), (2049, 130, 16), (5000, 17, 72), (20000, 3, 8),
         (40001, 300000, 9), (16384, 513, 520)]
 
 

@@ -15,7 +15,7 @@ def _c(*shape, dtype=torch.float32):
 def test_embedding():
     table, ids = _c(10, 8), _c(4, dtype=torch.int64)
     dy = _c(4, 8)
-    many, mdy = _c(600, dtype=torch.int64), _c(600, 8)
+    many, mdy = _c(1600, dtype=torch.int64), _c(1600, 8)
     for error, f in (
             (TypeError, lambda: ns.muon_embed(table.half(), ids)), (TypeError, lambda: ns.muon_embed(table, ids.short())),
             (TypeError, lambda: ns.muon_embed(table, ids.cpu())), (ValueError, lambda: ns.muon_embed(table[0], ids)),

@@ -63,7 +63,7 @@ def test_embed_refusals(kw, code):
 
 
 def _embed_grad(**kw):
-    a = dict(dy=1 << 20, dt=0, ids=P, bits=32, tokens=600, vocab=10, dim=8, scale=1.0, out=1 << 21, ot=1, acc=0, ws=1 << 22,
+    a = dict(dy=1 << 20, dt=0, ids=P, bits=32, tokens=1600, vocab=10, dim=8, scale=1.0, out=1 << 21, ot=1, acc=0, ws=1 << 22,
              wsb=1 << 20)
     a.update(kw)
     return _lib.lib().muon_embed_grad(a["dy"], a["dt"], a["ids"], a["bits"], a["tokens"], a["vocab"], a["dim"], a["scale"],
@@ -178,10 +178,10 @@ def test_valid_calls_without_a_device_are_unsupported():
 def test_workspace_sizes():
     assert ns.embed_grad_workspace_size(0, 10, 8) == 0 and ns.layer_norm_grad_workspace_size(0, 8) == 0
     # Sorted pairs twice, two partial rows a piece of 32 positions.
-    assert ns.embed_grad_workspace_size(1000, 100, 64) >= 16 * 1000 + 32 * 2 * 64 * 4
+    assert ns.embed_grad_workspace_size(2000, 100, 64) >= 16 * 2000 + 32 * 2 * 64 * 4
     assert ns.layer_norm_grad_workspace_size(50000, 24) >= 2 * 24 * 4
     # Few tokens and few rows need none.
-    assert ns.embed_grad_workspace_size(512, 100, 64) == 0 < ns.embed_grad_workspace_size(513, 100, 64)
+    assert ns.embed_grad_workspace_size(256, 100, 64) == 0 < ns.embed_grad_workspace_size(257, 100, 64)
     assert ns.layer_norm_grad_workspace_size(7, 4096) == 0
     with pytest.raises(ns.MuonNSError):
         ns.embed_grad_workspace_size(-1, 10, 8)
