@@ -247,7 +247,10 @@ extern "C" int muon_layer_norm(const void* x, int x_type, const void* weight, co
       int vec = min_vec(min_vec(norm_vec(dim, x, x_type), norm_vec(dim, y, x_type)), vec_of(dim, weight, w_type));
       if (bias) vec = min_vec(vec, vec_of(dim, bias, w_type));
       return with_norm_vec<T>(vec, [&](auto vc) {
-        return with_group(group_of(dim, kFwdPer), [&](auto gc) {
+        // Few rows leave threads to spare: a row takes four times as many, and
+        // its loads and sums are that much shorter.
+        const bool few = rows <= 2LL * sm_count();
+        return with_group(group_of(dim, few ? kFwdPer / 4 : kFwdPer), [&](auto gc) {
           constexpr int V = decltype(vc)::value, G = decltype(gc)::value;
           constexpr int T1 = G > kNormCta ? G : kNormCta;
           const long long grid = (rows + T1 / G - 1) / (T1 / G);

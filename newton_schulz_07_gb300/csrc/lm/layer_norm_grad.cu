@@ -26,6 +26,59 @@ constexpr int kRingSmem = 200 * 1024;
 constexpr int kFewCta = 512;  // CTA size for few rows
 constexpr int kFewSmem = sizeof(float) * 2 * kFewCta * kBwdPer;
 
+// One row of each group, from its units of x and dy (unit(k, c): those of the
+// thread's k-th unit, at column c): adds to the thread's dw and db and, after
+// the sums over the row, writes dx.  Every thread of the CTA takes part.
+//
+// With d = x - mean and e = dy d: dw += r e, db += dy, and the row's sums are
+// those of dy w and e w; xh mean(a xh) = r^2 d mean(e w).
+template <typename T, typename TW, int VEC, int G, typename C, typename U>
+__device__ __forceinline__ void grad_row(const U& unit, const TW* __restrict__ w, bool live, long long row, int dim,
+                                         float inv_dim, float mu, float r, T* dx, float2 (&dw)[C::kK][C::kP],
+                                         float2 (&db)[C::kK][C::kP], float (*red)[32]) {
+  const int tid = threadIdx.x & (G - 1);
+  float2 s1 = both(0.0f), s2 = both(0.0f);
+  if (live) {
+#pragma unroll
+    for (int k = 0; k < C::kK; ++k) {
+      const int c = C::first(k, tid);
+      if (c < dim) {
+        float2 xp[C::kP], gp[C::kP], wp[C::kP];
+        unit(k, c, xp, gp);
+        to_pairs<TW, C::kU>(C::load(w, c, dim), wp);
+#pragma unroll
+        for (int j = 0; j < C::kP; ++j) {
+          const float2 e = mul2(gp[j], add2(xp[j], both(-mu)));
+          dw[k][j] = fma2(e, both(r), dw[k][j]);
+          db[k][j] = add2(db[k][j], gp[j]);
+          s1 = fma2(gp[j], wp[j], s1);
+          s2 = fma2(e, wp[j], s2);
+        }
+      }
+    }
+  }
+  float sum[2] = {s1.x + s1.y, s2.x + s2.y};
+  group_sums<G, 2>(sum, red);
+  const float m1 = -r * (sum[0] * inv_dim), m2 = -r * (r * (r * (sum[1] * inv_dim)));
+  if (live) {
+#pragma unroll
+    for (int k = 0; k < C::kK; ++k) {
+      const int c = C::first(k, tid);
+      if (c < dim) {
+        float2 xp[C::kP], gp[C::kP], wp[C::kP];
+        unit(k, c, xp, gp);
+        to_pairs<TW, C::kU>(C::load(w, c, dim), wp);
+#pragma unroll
+        for (int j = 0; j < C::kP; ++j) {
+          const float2 d = add2(xp[j], both(-mu));
+          xp[j] = fma2(mul2(gp[j], both(r)), wp[j], fma2(d, both(m2), both(m1)));
+        }
+        C::store(dx + row * dim, c, dim, xp);
+      }
+    }
+  }
+}
+
 // part: fp32 [gridDim.x][2][dim], this CTA's dw and db.
 // FEW: the grid is one cluster, whose CTAs add their sums through each other's
 // shared memory (in rank order), so few rows take one launch and no workspace.
@@ -35,25 +88,26 @@ __global__ void __launch_bounds__(FEW ? kFewCta : (G > kNormCta ? G : kNormCta))
                    const float* __restrict__ rstd, long long rows, int dim, float inv_dim, T* dx,
                    float* __restrict__ part, float* __restrict__ dweight, float* __restrict__ dbias) {
   constexpr int kRows = (FEW ? kFewCta : (G > kNormCta ? G : kNormCta)) / G;
-  constexpr int kK = kBwdPer / VEC;
+  using C = Cols<VEC, G, kBwdPer>;
+  constexpr int kK = C::kK;
   __shared__ float red[2][2][32];
-  extern __shared__ float acc[];  // [kRows][2][dim], only with kRows > 1 or FEW
+  extern __shared__ __align__(16) float acc[];  // [kRows][2][dim], only with kRows > 1 or FEW
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int tid = threadIdx.x & (G - 1), grp = threadIdx.x / G;
-  float dw[kK][VEC] = {}, db[kK][VEC] = {};
+  float2 dw[kK][C::kP] = {}, db[kK][C::kP] = {};
   const long long stride = static_cast<long long>(gridDim.x) * kRows;
   int buf = 0;
-  Vec<T, VEC> xv[kK], gv[kK], xn[FEW ? kK : 1], gn[FEW ? kK : 1];
+  Vec<T, C::kU> xv[kK], gv[kK], xn[FEW ? kK : 1], gn[FEW ? kK : 1];
   float mu = 0.0f, r = 0.0f, mu_next = 0.0f, r_next = 0.0f;
   auto fetch = [&](long long row, auto& xs, auto& gs, float& m, float& q) {
     if (row >= rows) return;
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
-      const int c = (k * G + tid) * VEC;
+      const int c = C::first(k, tid);
       if (c < dim) {
-        xs[k] = load_global<T, VEC>(x + row * dim + c);
-        gs[k] = load_global<T, VEC>(dy + row * dim + c);
+        xs[k] = C::load(x + row * dim, c, dim);
+        gs[k] = C::load(dy + row * dim, c, dim);
       }
     }
     m = mean[row];
@@ -78,53 +132,21 @@ __global__ void __launch_bounds__(FEW ? kFewCta : (G > kNormCta ? G : kNormCta))
     } else {
       fetch(row, xv, gv, mu, r);
     }
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int c = (k * G + tid) * VEC;
-      if (live && c < dim) {
-        const Vec<TW, VEC> wv = load_global<TW, VEC>(w + c);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float g = to_f32(gv[k].v[j]), xh = (to_f32(xv[k].v[j]) - mu) * r;
-          const float a = g * to_f32(wv.v[j]);
-          dw[k][j] = fmaf(g, xh, dw[k][j]);
-          db[k][j] += g;
-          s1 += a;
-          s2 = fmaf(a, xh, s2);
-        }
-      }
-    }
-    float sum[2] = {s1, s2};
-    group_sums<G, 2>(sum, red[buf]);
-    const float m1 = sum[0] * inv_dim, m2 = sum[1] * inv_dim;
-#pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const int c = (k * G + tid) * VEC;
-      if (live && c < dim) {
-        const Vec<TW, VEC> wv = load_global<TW, VEC>(w + c);
-        float o[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float g = to_f32(gv[k].v[j]), xh = (to_f32(xv[k].v[j]) - mu) * r;
-          o[j] = r * (g * to_f32(wv.v[j]) - m1 - xh * m2);
-        }
-        store_global<T, VEC>(dx + row * dim + c, o);
-      }
-    }
+    const auto unit = [&](int k, int, float2(&xp)[C::kP], float2(&gp)[C::kP]) {
+      to_pairs<T, C::kU>(xv[k], xp);
+      to_pairs<T, C::kU>(gv[k], gp);
+    };
+    grad_row<T, TW, VEC, G, C>(unit, w, live, row, dim, inv_dim, mu, live ? r : 0.0f, dx, dw, db, red[buf]);
   }
   float* mine = FEW ? acc : part + static_cast<long long>(blockIdx.x) * 2 * dim;
   if (kRows > 1 || FEW) {
     // The groups hold the same columns: added in group order.
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
-      const int c = (k * G + tid) * VEC;
+      const int c = C::first(k, tid);
       if (c < dim) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          acc[(2 * grp) * dim + c + j] = dw[k][j];
-          acc[(2 * grp + 1) * dim + c + j] = db[k][j];
-        }
+        C::template store<true>(acc + (2 * grp) * dim, c, dim, dw[k]);
+        C::template store<true>(acc + (2 * grp + 1) * dim, c, dim, db[k]);
       }
     }
     __syncthreads();
@@ -137,13 +159,10 @@ __global__ void __launch_bounds__(FEW ? kFewCta : (G > kNormCta ? G : kNormCta))
   } else {
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
-      const int c = (k * G + tid) * VEC;
+      const int c = C::first(k, tid);
       if (c < dim) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          mine[c + j] = dw[k][j];
-          mine[dim + c + j] = db[k][j];
-        }
+        C::template store<true>(mine, c, dim, dw[k]);
+        C::template store<true>(mine + dim, c, dim, db[k]);
       }
     }
   }
@@ -152,17 +171,22 @@ __global__ void __launch_bounds__(FEW ? kFewCta : (G > kNormCta ? G : kNormCta))
     __syncthreads();
     if (ctas > 1) ptx::cluster_sync();
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < 2 * dim; i += ctas * blockDim.x) {
-      float s = 0.0f;
-      for (int r = 0; r < ctas; ++r) {
-        float v;
-        if (ctas > 1)
-          asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                       : "=f"(v)
-                       : "r"(ptx::mapa(ptx::smem_u32(&acc[i]), static_cast<uint32_t>(r))));
-        else
-          v = acc[i];
-        s += v;
+      float v[8];  // all loads in flight at once
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        v[r] = 0.0f;
+        if (r < ctas) {
+          if (ctas > 1)
+            asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                         : "=f"(v[r])
+                         : "r"(ptx::mapa(ptx::smem_u32(&acc[i]), static_cast<uint32_t>(r))));
+          else
+            v[r] = acc[i];
+        }
       }
+      float s = v[0];
+#pragma unroll
+      for (int r = 1; r < 8; ++r) s += v[r];
       if (i < dim)
         dweight[i] = s;
       else if (dbias != nullptr)
@@ -229,51 +253,11 @@ __global__ void __launch_bounds__(G > kNormCta ? G : kNormCta, G > kNormCta ? 1 
     if (kWords) group_barrier<G>();
     const T* xs = mine_x + st * turn + (kWords ? row_shift(x + row * dim) : 0);
     const T* gs = mine_x + st * turn + to_dy + (kWords ? row_shift(dy + row * dim) : 0);
-    // With d = x - mean and e = dy d: dw += r e, db += dy, and the row's sums
-    // of dy w and e w.
-    float2 s1 = both(0.0f), s2 = both(0.0f);
-    if (live) {
-#pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        const int c = C::first(k, tid);
-        if (c < dim) {
-          float2 xp[kP], gp[kP], wp[kP];
-          to_pairs<T, C::kU>(C::template load<true>(xs, c, dim), xp);
-          to_pairs<T, C::kU>(C::template load<true>(gs, c, dim), gp);
-          to_pairs<TW, C::kU>(C::load(w, c, dim), wp);
-#pragma unroll
-          for (int j = 0; j < kP; ++j) {
-            const float2 e = mul2(gp[j], add2(xp[j], both(-mu)));
-            dw[k][j] = fma2(e, both(r), dw[k][j]);
-            db[k][j] = add2(db[k][j], gp[j]);
-            s1 = fma2(gp[j], wp[j], s1);
-            s2 = fma2(e, wp[j], s2);
-          }
-        }
-      }
-    }
-    float sum[2] = {s1.x + s1.y, s2.x + s2.y};
-    group_sums<G, 2>(sum, red[st]);
-    // xh mean(a xh) = r^2 d mean(e w).
-    const float m1 = -r * (sum[0] * inv_dim), m2 = -r * (r * (r * (sum[1] * inv_dim)));
-    if (live) {
-#pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        const int c = C::first(k, tid);
-        if (c < dim) {
-          float2 xp[kP], gp[kP], wp[kP];
-          to_pairs<T, C::kU>(C::template load<true>(xs, c, dim), xp);
-          to_pairs<T, C::kU>(C::template load<true>(gs, c, dim), gp);
-          to_pairs<TW, C::kU>(C::load(w, c, dim), wp);
-#pragma unroll
-          for (int j = 0; j < kP; ++j) {
-            const float2 d = add2(xp[j], both(-mu));
-            xp[j] = fma2(mul2(gp[j], both(r)), wp[j], fma2(d, both(m2), both(m1)));
-          }
-          C::store(dx + row * dim, c, dim, xp);
-        }
-      }
-    }
+    const auto unit = [&](int, int c, float2(&xp)[C::kP], float2(&gp)[C::kP]) {
+      to_pairs<T, C::kU>(C::template load<true>(xs, c, dim), xp);
+      to_pairs<T, C::kU>(C::template load<true>(gs, c, dim), gp);
+    };
+    grad_row<T, TW, VEC, G, C>(unit, w, live, row, dim, inv_dim, mu, r, dx, dw, db, red[st]);
     if (kWords) group_barrier<G>();  // the row has been read before its buffer is copied to
   }
   copy_wait<0>();
@@ -394,12 +378,12 @@ bool use_ring(int dim, int x_type, int vec, const void* x, const void* dy) {
   return dim <= kRingMax && (vec * type_size(x_type) >= 4 || words) && ring_smem(dim, x_type) <= kRingSmem;
 }
 
-// CTAs of the one cluster that few rows take (1, 2, 4 or 8), or 0.  Up to 9
-// turns of it: a turn is about 1.3 us, the second launch and the workspace it
-// saves about 4 on the device and 5 to issue.
+// CTAs of the one cluster that few rows take (1, 2, 4 or 8), or 0.  Up to 4
+// turns of it: 517 rows of 768 bf16 take 9 turns and 21 us on the device,
+// against 9 us by the two launches, which take 6 us longer to issue.
 int few_ctas(long long rows, int dim) {
   const int g = group_of(dim, kBwdPer);
-  if (g > kFewCta || rows > 9LL * 8 * (kFewCta / g)) return 0;
+  if (g > kFewCta || rows > 4LL * 8 * (kFewCta / g)) return 0;
   int n = 1;
   while (n < 8 && n * (kFewCta / g) < rows) n *= 2;
   return n;
