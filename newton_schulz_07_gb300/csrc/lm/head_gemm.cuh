@@ -240,6 +240,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------ producer
+      // The operands were written by other kernels' ordinary stores.
+      ptx::fence_proxy_async_global();
       int stage = 0, fills = 0;
       uint32_t phase = 0;
       bool ok = true;
