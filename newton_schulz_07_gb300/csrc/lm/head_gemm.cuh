@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
   // Stages this CTA has asked to be filled, and (in the pair's first CTA) the
   // stages and accumulators its MMAs have committed.
   __shared__ int fills_sh, stages_sh, units_sh;
+  __shared__ int peer_abort_sh;  // the other CTA of the pair gave up
 
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
     }
     ptx::mbar_init(mma_done, 1);
     *abort_flag = 0;
-    fills_sh = stages_sh = units_sh = 0;
+    fills_sh = stages_sh = units_sh = peer_abort_sh = 0;
     ptx::fence_barrier_init();
     ptx::prefetch_tensormap(&P.tmA);
     ptx::prefetch_tensormap(&P.tmB);
@@ -281,6 +282,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
         }
       }
       fills_sh = fills;
+      // The last release of each stage is awaited here, so that after a full
+      // run no commit is on its way to this CTA's barriers when it leaves.
+      for (int i = fills > kHeadStages ? fills - kHeadStages : 0; ok && i < fills; ++i)
+        ok = detail::wait_bounded<true>(empty(i % kHeadStages), (i / kHeadStages) & 1, abort_flag, err, P.budget);
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
@@ -504,13 +509,22 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  if (threadIdx.x == 0 && *abort_flag)
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(
+                     ptx::mapa(ptx::smem_u32(&peer_abort_sh), static_cast<uint32_t>(crank ^ 1))),
+                 "r"(1)
+                 : "memory");
+  // Neither CTA leaves while the other may still address it.
   ptx::cluster_sync();
-  if (warp == 0 && lane == 0) {
-    // Nothing may be on its way to a CTA that leaves.  After a full run all of
-    // this has happened; after a wait that ran out the two CTAs may have asked
-    // for different numbers of fills.  Copies are counted on the first CTA's
-    // barriers: it expects the other's bytes alone for fills of its own that
-    // are missing, and the other stands in for its missing ones.
+  // (The same in both CTAs: neither flag changes any more.)
+  const bool gave_up = *abort_flag || *static_cast<volatile int*>(&peer_abort_sh);
+  if (gave_up && warp == 0 && lane == 0) {
+    // Nothing may be on its way to a CTA that leaves.  After a full run every
+    // arrival has been awaited by the role that it was for; after a wait that
+    // ran out the two CTAs may have asked for different numbers of fills.
+    // Copies are counted on the first CTA's barriers: it expects the other's
+    // bytes alone for fills of its own that are missing, and the other stands
+    // in for its missing ones.
     auto remote = [](const int* p, int rank) {
       int v;
       asm volatile("ld.shared::cluster.s32 %0, [%1];"
@@ -539,8 +553,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
       detail::drain_wait<true>(empty(i % kHeadStages), (i / kHeadStages) & 1, drain);
     for (int i = units > 2 ? units - 2 : 0; i < units; ++i) detail::drain_wait<true>(tfull(i & 1), (i >> 1) & 1, drain);
   }
-  __syncthreads();
-  ptx::cluster_sync();
+  if (gave_up) {
+    __syncthreads();
+    ptx::cluster_sync();
+  }
   if (warp == 0) {
     __syncwarp();
     ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
