@@ -148,12 +148,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
   __shared__ int peer_abort_sh;  // the other CTA of the pair gave up
 
   ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  // Read first, so that the setup below hides it.
-  const int4 ctl = *reinterpret_cast<const int4*>(P.ctl);
-  static_assert(kCtlCount == 1 && kCtlSplits == 2 && kCtlRedo == 3, "control words");
   // Nothing to do again: the whole grid leaves before it sets anything up.
-  if (MODE == kLogits && P.redo != nullptr && ctl.w == 0) return;
+  if (MODE == kLogits && P.redo != nullptr) {
+    ptx::griddep_wait();
+    if (P.ctl[kCtlRedo] == 0) return;
+  }
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int crank = static_cast<int>(ptx::cluster_ctarank());
@@ -197,6 +196,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem_base = tmem_base_sh;
+  // The set-up above touches this CTA's own memory alone and runs beside the
+  // end of the kernel before.
+  ptx::griddep_wait();
+  const int4 ctl = *reinterpret_cast<const int4*>(P.ctl);
+  static_assert(kCtlCount == 1 && kCtlSplits == 2, "control words");
 
   // The tile space: `splits` times pair rows x column tiles, split-major, so
   // that tiles running together read the same part of a split contraction.
