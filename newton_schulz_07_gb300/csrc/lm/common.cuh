@@ -77,6 +77,8 @@ __device__ __forceinline__ void store_global(T* p, const float (&f)[VEC]) {
     store_vec<T, VEC>(p, f);
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Token id at `t`, or -1 if it names no row of the table.
 __device__ __forceinline__ long long load_id(const void* ids, int ids64, long long t, long long vocab) {
   const long long v = ids64 ? static_cast<const long long*>(ids)[t]

@@ -50,30 +50,8 @@ constexpr size_t kRankSmem = sizeof(unsigned int) * kRankTokens;
 __device__ __forceinline__ int rank_tokens(const SortBy& by, int b, unsigned int* keys, unsigned int* key_out) {
   __shared__ int part[32][33];
   const int n = static_cast<int>(by.tokens), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const unsigned int none = static_cast<unsigned int>(none_of(by));
   const int pad = (n + 127) / 128 * 128;
-  int live = 0;
-  for (int i = tid; i < pad; i += 1024) {
-    const unsigned int k = i < n ? sort_key(by, i) : 0xFFFFFFFFu;  // past every key
-    keys[i] = k;
-    live += k < none ? 1 : 0;
-  }
-  if (b == 0 && by.count != nullptr) {
-    part[warp][lane] = live;
-    __syncthreads();
-    int v = part[lane][warp];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    __syncthreads();
-    if (lane == 0) part[0][warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-      v = part[0][lane];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-      if (lane == 0) *by.count = v;
-    }
-  }
+  for (int i = tid; i < pad; i += 1024) keys[i] = i < n ? sort_key(by, i) : 0xFFFFFFFFu;  // past every key
   __syncthreads();
   const int i0 = b * kRankBlock, i = i0 + lane;
   const unsigned int mine = i < n ? keys[i] : 0u;
@@ -97,11 +75,20 @@ __device__ __forceinline__ int rank_tokens(const SortBy& by, int b, unsigned int
   }
   part[warp][lane] = below;
   __syncthreads();
-  int r = part[lane][warp];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
+  const int r = __reduce_add_sync(0xFFFFFFFFu, part[lane][warp]);
   *key_out = __shfl_sync(0xFFFFFFFFu, mine, warp);
   return r;
+}
+
+// How many of at most kRankTokens ids name a row, by the 1024 threads of a CTA.
+__device__ __forceinline__ int count_live(const SortBy& by) {
+  int live = 0;
+#pragma unroll
+  for (int k = 0; k < kRankTokens / 1024; ++k) {
+    const int i = k * 1024 + static_cast<int>(threadIdx.x);
+    live += __syncthreads_count(i < by.tokens && sort_key(by, i) < none_of(by) ? 1 : 0);
+  }
+  return live;
 }
 
 // Rows of a table to be set to zero where no token names them.

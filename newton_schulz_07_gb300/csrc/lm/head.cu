@@ -126,23 +126,36 @@ __device__ __forceinline__ void start_row(const HeadRows& R, const bf16* __restr
   }
 }
 
-// Up to kRankTokens tokens: a CTA ranks 32 and starts their rows.
+// Up to kRankTokens tokens: a CTA ranks 32 and starts their rows; the last one
+// counts the live tokens and chooses the splits.
 __global__ void __launch_bounds__(1024)
     head_rank(const SortBy by, const HeadRows R, const bf16* __restrict__ h, const bf16* __restrict__ W,
               bf16* __restrict__ hc, int pair_rows, int split_kb, unsigned long long* __restrict__ sorted) {
   extern __shared__ __align__(16) unsigned int keys[];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  unsigned int key;
-  const int p = rank_tokens(by, blockIdx.x, keys, &key);
+  if (blockIdx.x == gridDim.x - 1) {
+    const int count = count_live(by);
+    if (threadIdx.x == 0) R.ctl[kCtlCount] = count;
+    start_call(R, count, pair_rows, split_kb);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
   const long long t = static_cast<long long>(blockIdx.x) * kRankBlock + (threadIdx.x >> 5);
   if (t < by.tokens) {
-    if ((threadIdx.x & 31) == 0) sorted[p] = (static_cast<unsigned long long>(key) << 32) | t;
-    if (key < none_of(by)) start_row(R, h, W, hc, p, t);
+    // The rows are on their way to L2 while the tokens are ranked.
+    const long long id = load_id(by.ids, by.ids64, t, by.vocab);
+    if (id >= 0 && id != by.skip)
+      for (int c = lane * 64; c < R.dim; c += 2048) {
+        prefetch_l2(h + t * R.dim + c);
+        prefetch_l2(W + id * R.dim + c);
+      }
   }
-  if (blockIdx.x == 0) {
-    __syncthreads();
-    start_call(R, *static_cast<volatile int*>(by.count), pair_rows, split_kb);
+  unsigned int key;
+  const int p = rank_tokens(by, blockIdx.x, keys, &key);
+  if (t < by.tokens) {
+    if (lane == 0) sorted[p] = (static_cast<unsigned long long>(key) << 32) | t;
+    if (key < none_of(by)) start_row(R, h, W, hc, p, t);
   }
 }
 
@@ -281,23 +294,20 @@ __global__ void __launch_bounds__(256)
       for (int j = 0; j < 8; ++j) o[j] += v.v[j];
     }
   };
-  auto finish = [&](long long p, int c, const float (&o)[8]) {
-    const unsigned int token = static_cast<unsigned int>(R.sorted[p]);
-    float out[8] = {};
-    if (p < count) {
-      const long long t = load_id(R.targets, R.ids64, token, R.vocab);
-      const Vec<bf16, 8> w = load_vec<bf16, 8>(W + t * R.dim + c);
-      const float f = R.scale[p], k = R.coef[p];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) out[j] = fmaf(f, o[j], k * to_f32(w.v[j]));
-    }
-    store_vec<bf16, 8>(dh + static_cast<long long>(token) * R.dim + c, out);
-  };
   const long long i = SHARED ? blockIdx.x : static_cast<long long>(blockIdx.x) * 8 + warp;
   if (i >= items) return;
   const long long p = i / slices;
   const int c = static_cast<int>(i - p * slices) * 256 + lane * 8;
   const bool live = p < count && c < R.dim;
+  // The target's row is asked for before the splits are added.
+  const unsigned int token = static_cast<unsigned int>(R.sorted[p]);
+  Vec<bf16, 8> w = {};
+  float f = 0.0f, k = 0.0f;
+  if (live && (!SHARED || warp == 0)) {
+    w = load_vec<bf16, 8>(W + load_id(R.targets, R.ids64, token, R.vocab) * R.dim + c);
+    f = R.scale[p];
+    k = R.coef[p];
+  }
   float o[8] = {};
   if (live) add(p, c, SHARED ? splits * warp / 8 : 0, SHARED ? splits * (warp + 1) / 8 : splits, o);
   if (SHARED) {
@@ -310,7 +320,12 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] += red[g][j * 32 + lane];
   }
-  if (c < R.dim) finish(p, c, o);
+  if (c >= R.dim) return;
+  float out[8] = {};
+  if (live)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) out[j] = fmaf(f, o[j], k * to_f32(w.v[j]));
+  store_vec<bf16, 8>(dh + static_cast<long long>(token) * R.dim + c, out);
 }
 
 // -------------------------------------------------------------------- host --
@@ -477,7 +492,7 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
   // The losses alone need no order among the live tokens.
   const SortBy by = {C.targets, C.ids64, N, V, C.skip, grad ? 0 : 1, R.ctl + kCtlCount};
   if (N <= kRankTokens) {
-    MNS_TRY(mns::launch_pdl(head_rank, dim3(static_cast<unsigned>((N + kRankBlock - 1) / kRankBlock)), dim3(1024),
+    MNS_TRY(mns::launch_pdl(head_rank, dim3(static_cast<unsigned>((N + kRankBlock - 1) / kRankBlock + 1)), dim3(1024),
                             kRankSmem, C.stream, by, R, C.h, C.W, hc, static_cast<int>(pair_rows), split_kb,
                             reinterpret_cast<unsigned long long*>(at(L.sums + L.sum.sorted))));
   } else {
@@ -523,13 +538,15 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
     F.v0 = kept * L.piece;
     F.vp = static_cast<int>(width(kept));
   }
-  const unsigned finish_grid = static_cast<unsigned>(N < 152 * 16 ? N : 152 * 16);
   for (int again = 0; again < 2; ++again) {
     for (long long j = 0; j < L.pieces; ++j) {
       const int s = logits(j, true, grad && j == kept, again ? R.redo : nullptr);
       if (s != MUON_NS_OK) return s;
     }
     F.again = again;
+    // (The second pass mostly has nothing to do: CTAs that start at once.)
+    const long long most = 152 * (again ? 4 : 16);
+    const unsigned finish_grid = static_cast<unsigned>(N < most ? N : most);
     MNS_TRY(mns::launch_pdl(head_finish, dim3(finish_grid), dim3(128), 0, C.stream, R, F));
   }
   if (!grad) return MUON_NS_OK;
