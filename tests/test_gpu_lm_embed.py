@@ -109,6 +109,25 @@ def test_gradient(tokens, vocab, dim, types, accumulate):
         assert torch.equal(got.cpu()[count == 0], start[count == 0])
 
 
+@pytest.mark.parametrize("tokens,vocab,dim", [(257, 50257, 256), (1023, 20011, 601), (4096, 700, 20000), (4097, 30000, 401),
+                                              (300, 900000, 40)])
+@pytest.mark.parametrize("to", [torch.float32, torch.bfloat16])
+def test_gradient_into_large_tables(tokens, vocab, dim, to):
+    # Tables whose zeroing takes longer than ranking the tokens, on both sides
+    # of the sizes that divide it; every row is written, whatever it held.
+    dy, ids = _values((tokens, dim), 31, torch.bfloat16).cuda(), _ids(tokens, vocab, 32).cuda()
+    got = torch.full((vocab, dim), float("nan"), dtype=to, device="cuda")
+    ns.muon_embed_grad(dy, ids, vocab, dtable=got)
+    ok = (ids >= 0) & (ids < vocab)
+    rows, at = torch.unique(ids[ok], return_inverse=True)
+    z = torch.zeros((len(rows), dim), dtype=torch.float64, device="cuda")
+    exact, size = z.index_add(0, at, dy[ok].double()), z.index_add(0, at, dy[ok].double().abs())
+    bound = (torch.bincount(at)[:, None] + 2) * E * size
+    assert torch.all((got[rows].double() - exact).abs() <= bound + U[to] * (exact.abs() + bound) + TINY)
+    got[rows] = 0
+    assert not got.any()
+
+
 @pytest.mark.parametrize("tokens", [33, 3000, 70000])
 def test_gradient_of_one_token_repeated(tokens):
     # One row takes every token: a sum over pieces, sorted by one CTA or several.
