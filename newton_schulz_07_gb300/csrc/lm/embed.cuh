@@ -25,7 +25,7 @@ struct SortBy {
   long long tokens, vocab;
   long long skip;  // an id to be taken as naming no row (-1: none more)
   int presence;    // sort by whether an id names a row alone (key 0: it does, 1: it does not)
-  int* count;      // optional, device: how many do
+  int* count;      // optional, device: how many do (written by a sort of more than kRankTokens)
 };
 
 // Key of an id that names no row.

@@ -513,8 +513,8 @@ int muon_layer_norm_grad(const void* dy, const void* x, int x_type, const void* 
                                                        mean, rstd, rows, dim, inv, op, part, dweight, dbias));
             }
           }
-          return status_of(mns::launch_pdl(layer_norm_bwd<T, TW, V, G, false>, dim3(parts), dim3(T1), smem, stream, gp, xp, wp, mean, rstd, rows, dim, inv, op, part,
-                                           dweight, dbias));
+          return status_of(mns::launch_pdl(layer_norm_bwd<T, TW, V, G, false>, dim3(parts), dim3(T1), smem, stream, gp,
+                                           xp, wp, mean, rstd, rows, dim, inv, op, part, dweight, dbias));
         });
       });
     });
