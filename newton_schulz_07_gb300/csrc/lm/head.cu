@@ -4,19 +4,25 @@
 //   z = h W^T, loss_n = log sum_v exp z_nv - z_nt, p = softmax(z),
 //   dz_nv = g_n (p_nv - [v = t_n]), dh = dz W, dW = dz^T h.
 //
-// Every row is referred to its target's own logit c_n = z_nt, one dot product
-// known before the large one: with e_nv = exp(z_nv - c_n) and s_n = sum_v e_nv,
-//   loss_n = log s_n,  dz_nv = (g_n / s_n) e_nv for v != t,
-//   dz_nt = -g_n (s_n - e_nt) / s_n.
+// Every row is referred to its target's logit c_n, one dot product known before
+// the large one: with e_nv = exp(z_nv - c_n), s_n the sum of e_nv over v != t and
+// e_nt the target's own (1, but where the reference is another),
+//   loss_n = log(1 + s_n / e_nt),  dz_nv = g_n e_nv / (s_n + e_nt) for v != t,
+//   dz_nt = -g_n s_n / (s_n + e_nt).
 // So the large product's epilogue takes exponentials and their sum in one
 // pass with no running maximum, and e needs no second pass once s is known:
-// g_n / s_n is a factor of row n of dh, and of row n of h in dW.  The target's
-// own term, which cancels and would lose its digits in bf16, is set to zero in
-// e and added to dh and dW in fp32.  s_n >= e_nt = 1 by construction, so only a
-// logit far above the target's (a loss above log kTopSum = 44) can leave the
-// range: such rows take their largest logit as reference and the tiles that
-// hold them are computed again; the launches that do so leave at once when
-// there are none.
+// g_n / (s_n + e_nt) is a factor of row n of dh, and of row n of h in dW.
+//
+// The target stays out of s and of the stored e: a token with p near 1 has its
+// loss and its target's term, both about 1 - p, to the relative accuracy of the
+// logits' differences.  (In the sum, the target's exponential is 1 and the
+// difference of two orders of summation: losses down to -6e-4 at dim 4096 and
+// logits of 40.)  The target's term is added to dh and dW in fp32.
+//
+// Only a logit far above the target's (a loss above log kTopSum = 44) can leave
+// the range: such rows take their largest logit as reference and the tiles that
+// hold them are computed again; the launches that do so leave at once when there
+// are none.
 //
 // Tokens without a loss (target out of range or ignored) are sorted to the
 // end and take no part in the products.  The rest is sorted by target, so the
@@ -45,6 +51,9 @@ namespace lm {
 namespace {
 
 constexpr float kTopSum = 1.8446744e19f;  // 2^64
+// Below it (only where the reference is the largest logit) the target's
+// exponential may have lost digits, or be zero.
+constexpr float kLeastTarget = 5.421011e-20f;  // 2^-64
 constexpr int kHeadPairs = 76;            // CTA pairs the splits are chosen for
 // Pair rows walked together: of e or W as many are read again as there are
 // bands.  (8 to 32 for the logits differ by half a percent at 8192 tokens.)
@@ -85,10 +94,11 @@ struct HeadRows {
   int dim;
   int* ctl;
   int* redo;   // per pair row
-  float* zt;   // target's logit
+  int* col;    // target
+  float* zt;   // its logit
   float* ref;  // reference of the exponentials
-  float* scale;  // g / s
-  float* coef;   // -g (s - e_t) / s
+  float* scale;  // g / (s + e_t)
+  float* coef;   // -g s / (s + e_t)
 };
 
 // Clears the control words and chooses dh's splits: one CTA, all threads.
@@ -103,7 +113,7 @@ __device__ __forceinline__ void start_call(const HeadRows& R, int count, int pai
   }
 }
 
-// Row p of the compact copy of h, and its target's logit: one warp.
+// Row p of the compact copy of h, its target and the target's logit: one warp.
 __device__ __forceinline__ void start_row(const HeadRows& R, const bf16* __restrict__ h, const bf16* __restrict__ W,
                                           bf16* __restrict__ hc, long long p, long long token) {
   const int lane = threadIdx.x & 31;
@@ -121,6 +131,7 @@ __device__ __forceinline__ void start_row(const HeadRows& R, const bf16* __restr
   }
   const float z = warp_sum(((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7])));
   if (lane == 0) {
+    R.col[p] = static_cast<int>(t);
     R.zt[p] = z;
     R.ref[p] = z;
   }
@@ -179,10 +190,7 @@ struct HeadFinish {
   float* loss;         // per token
   // gradient
   const bf16* hc;
-  bf16* hs;   // (g / s) h, rows up to a multiple of 64 zero
-  bf16* e;    // the piece held, its first column v0 and its columns
-  long long lde, v0;
-  int vp;
+  bf16* hs;   // scale h, rows up to a multiple of 64 zero
 };
 
 // A CTA a sorted position: joins the row's sums in a fixed order, and from
@@ -208,7 +216,6 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
     if (F.again && R.redo[p / kHeadRows] == 0) continue;
     // Loaded before the sums are joined; all independent of one another.
     const float zt = R.zt[p], c = R.ref[p];
-    const long long t = load_id(R.targets, R.ids64, token, R.vocab);
     const float g = F.hs == nullptr ? 0.0f : F.dloss != nullptr ? F.dloss[token] : 1.0f / static_cast<float>(count);
     const bool one = F.hs != nullptr && R.dim <= 1024;  // a vector a thread
     Vec<bf16, 8> x = {};
@@ -232,6 +239,8 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
     __syncthreads();
     s = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
     mx = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
+    // The target's exponential, as the epilogue takes the others'.
+    const float et = exp2_approx(fmaf(zt, kLog2e, -(c * kLog2e)));
     if (!F.again && !(s <= kTopSum)) {  // out of range, or not a number
       if (tid == 0) {
         R.ref[p] = mx;
@@ -240,13 +249,12 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
       }
       continue;
     }
-    if (tid == 0) F.loss[token] = logf(s) + (c - zt);
+    if (tid == 0) F.loss[token] = et >= kLeastTarget ? log1pf(s / et) : logf(s + et) + (c - zt);
     if (F.hs == nullptr) continue;
-    const float f = g / s;
+    const float f = g / (s + et);
     if (tid == 0) {
       R.scale[p] = f;
-      R.coef[p] = -g * ((s - expf(zt - c)) / s);
-      if (t >= F.v0 && t < F.v0 + F.vp) F.e[p * F.lde + (t - F.v0)] = 0;
+      R.coef[p] = -g * (s / (s + et));
     }
     // hs is the MMAs' bf16 operand: one more rounding, up to 2^-8, in each term of
     // dW but the targets', which are added in fp32.
@@ -258,17 +266,6 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
       store_vec<bf16, 8>(F.hs + p * R.dim + col, o);
     }
   }
-}
-
-// The targets' terms of a piece that was computed again.
-__global__ void __launch_bounds__(256)
-    head_clear_targets(const HeadRows R, bf16* __restrict__ e, long long lde, long long v0, int vp) {
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  const long long p = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  if (p >= R.ctl[kCtlCount]) return;
-  const long long t = load_id(R.targets, R.ids64, static_cast<unsigned int>(R.sorted[p]), R.vocab);
-  if (t >= v0 && t < v0 + vp) e[p * lde + (t - v0)] = 0;
 }
 
 // dh[token] = scale (sum of the splits, in order) + coef W[target].  An item is
@@ -338,7 +335,7 @@ __global__ void __launch_bounds__(256)
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 struct HeadLayout {
-  size_t redo, zt, ref, scale, coef, stat, sums, slot, hc, hs, addend, e, part, total;
+  size_t redo, col, zt, ref, scale, coef, stat, sums, slot, hc, hs, addend, e, part, total;
   SumLayout sum;
   long long piece, pieces, lde, part_rows;
   int halves;
@@ -373,6 +370,7 @@ HeadLayout head_layout(long long tokens, long long vocab, int dim, bool grad, in
   };
   const size_t n_tok = static_cast<size_t>(tokens);
   L.redo = take(4 * static_cast<size_t>(pair_rows));
+  L.col = take(4 * n_tok);
   L.zt = take(4 * n_tok);
   L.ref = take(4 * n_tok);
   L.scale = take(4 * n_tok);
@@ -483,6 +481,7 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
   R.dim = D;
   R.ctl = reinterpret_cast<int*>(ws);
   R.redo = reinterpret_cast<int*>(at(L.redo));
+  R.col = reinterpret_cast<int*>(at(L.col));
   R.zt = f32_at(L.zt);
   R.ref = f32_at(L.ref);
   R.scale = f32_at(L.scale);
@@ -516,6 +515,8 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
     P.vp = static_cast<int>(width(j));
     P.group = kLogitsGroup;
     P.ref = R.ref;
+    P.target = R.col;
+    P.v0 = j * L.piece;
     P.stat = stats ? reinterpret_cast<float2*>(at(L.stat)) : nullptr;
     P.stat_ld = L.halves;
     P.stat0 = static_cast<int>(j * L.piece / kHeadHalf);
@@ -538,10 +539,6 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
   if (grad) {
     F.hc = hc;
     F.hs = hs;
-    F.e = e;
-    F.lde = L.lde;
-    F.v0 = kept * L.piece;
-    F.vp = static_cast<int>(width(kept));
   }
   for (int again = 0; again < 2; ++again) {
     for (long long j = 0; j < L.pieces; ++j) {
@@ -566,8 +563,6 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
     if (i > 0) {
       const int s = logits(j, false, true, nullptr);
       if (s != MUON_NS_OK) return s;
-      MNS_TRY(mns::launch_pdl(head_clear_targets, dim3(static_cast<unsigned>((N + 255) / 256)), dim3(256), 0, C.stream,
-                              R, e, L.lde, v0, vp));
     }
     HeadGemm P = G;
     P.vp = vp;

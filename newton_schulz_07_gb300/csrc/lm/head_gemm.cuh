@@ -3,7 +3,8 @@
 // With e = exp(h W^T - ref) of the live tokens (compact rows, `count` of them)
 // and one piece of the vocabulary,
 //   kLogits  z = h W^T (both operands K-major); the epilogue takes e, its row
-//            sums and the rows' largest z, and stores e in bf16;
+//            sums and the rows' largest z, and stores e in bf16, all without
+//            the rows' targets;
 //   kDh      e W (e K-major, W MN-major) in fp32, split over the vocabulary
 //            where there are few output tiles; splits go to rows of their own,
 //            later pieces are added by bulk reductions;
@@ -61,6 +62,7 @@ struct HeadGemm {
   int sectors;  // its rows start on 32 bytes
   // kLogits
   const float* ref;   // per row
+  const int* target;  // per row: its column of the whole vocabulary
   float2* stat;       // [rows][stat_ld]: (largest z, sum of e) of 128 columns; may be null
   int stat_ld, stat0; // stat0: the piece's first
   int store;          // write e
@@ -71,6 +73,7 @@ struct HeadGemm {
   const float* addend;         // fp32 [rows][dim], compact
   const int* slot;             // row of a vocabulary row's addend: one if sorted[slot] has its key
   const unsigned long long* sorted;
+  // kLogits, kDw*
   long long v0;                // first vocabulary row of the piece
   long long budget;
 };
@@ -375,9 +378,13 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
       // What the rows need besides the product, fetched before the wait.
       float cl = 0.0f;
       bool live = false;
+      int target = -1;  // among the warp's columns, if it is there
       if (MODE == kLogits) {
         live = row < count;
-        if (live) cl = P.ref[row] * kLog2e;
+        if (live) {
+          cl = P.ref[row] * kLog2e;
+          target = P.target[row] - static_cast<int>(P.v0) - col0;
+        }
       }
       const float* addend = nullptr;
       if (MODE >= kDwBf16) {
@@ -422,22 +429,31 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm(const __grid_consta
         if (MODE == kLogits) {
           // Columns past the piece hold zero, not a logit: no part of the sums.
           const int n = cols - gj;
+          // Nor is the target's: 1 - p is the sum of the others, and would be
+          // lost in rounding beside it.  (Rows are sorted by target where there
+          // is a gradient; few chunks hold any.)
+          const int hit = target - cc * 32;
+          if (__any_sync(0xFFFFFFFFu, static_cast<unsigned>(hit) < 32u)) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (hit == j) v[j] = 0xFF800000u;  // -infinity
+          }
           float f[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const float z = j < n ? __uint_as_float(v[j]) : -INFINITY;
             mx = fmaxf(mx, z);
             // One fused multiply-add in the exponent: the rounding of cl moves
-            // the whole row's reference by 2^-24 of itself and cancels in the
-            // gradient.
+            // the whole row's reference by 2^-24 of itself, the target's
+            // exponential (head_finish) with it, and cancels in their ratios.
             f[j] = exp2_approx(fmaf(z, kLog2e, -cl));
             s4[j & 3] += f[j];
           }
           if (P.store) {
             // e is rounded to bf16 here, the MMAs' operand type: a relative
             // error of up to 2^-8 in each term of sums over many; the target's
-            // term, which cancels, is left out of e and added in fp32.  Rows
-            // past the live tokens are zero.
+            // term, the sum of all others, is added in fp32.  Rows past the
+            // live tokens are zero.
             if (row < P.rows) {
               uint32_t w[16];
 #pragma unroll

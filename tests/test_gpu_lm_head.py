@@ -284,3 +284,49 @@ def test_a_wait_that_runs_out_reports_and_returns():
     got = ns.muon_head_loss_grad(h, w, t, workspace=ws)
     assert ns.read_error(ws) == 0
     assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def _confident(n, v, d, level, seed):
+    """Dense rows whose target holds about 1 - `level` of the probability; the
+    logits are shifted together, so that the targets' are 25 to 45 and no
+    power of two.  Every target is a row of its own."""
+    g = torch.Generator().manual_seed(seed)
+    w = torch.randn((v, d), generator=g)
+    common = torch.randn(d, generator=g)
+    t = torch.randperm(v, generator=g)[:n]
+    want = math.log(v / level)
+    h = w[t] * (want / w[t].square().sum(1, keepdim=True)) + common * (17.3 / common.square().sum())
+    return h.bfloat16(), (w + common).bfloat16(), t
+
+
+@pytest.mark.parametrize("level", [1e-3, 1e-5, 1e-7])
+@pytest.mark.parametrize("n,v,d", [(40, 1500, 768), (300, 1003, 2048), (70, 5003, 4096), (4200, 5003, 256)])
+@pytest.mark.parametrize("pieces", [1, 2])
+def test_confident_tokens_of_dense_rows(n, v, d, level, pieces):
+    # With 1 - p small, the loss is 1 - p to first order and the target's term
+    # -g (1 - p): both as exact, relative to themselves, as the gaps between the
+    # logits are.  A gap is off by 2 dz, an exponential of it by 8 e and the
+    # rounding of its argument (e times the gap, below 100), their sum by 64 e:
+    # `off` of 1 - p, in all.
+    h, w, t = _confident(n, v, d, level, n + d)
+    hd, wd, tc = h.double().cuda(), w.double().cuda(), t.cuda()
+    z = hd @ wd.T
+    dz = (_acc(d) * (hd.abs() @ wd.abs().T)).amax(1, keepdim=True)
+    off = 1.1 * (2 * dz + 256 * E)
+    zt = z.gather(1, tc[:, None])
+    hot = torch.zeros_like(z).scatter_(1, tc[:, None], 1.0)
+    rest = (torch.exp(z - zt) * (1 - hot)).sum(1, keepdim=True)  # (1 - p) / p, without cancellation
+    loss = torch.log1p(rest)
+    assert level / 10 < float(rest.median()) < level * 10 and float(off.max()) < 0.01
+    p = torch.exp(z - zt) * (1 - hot) / (1 + rest)
+    want = [loss[:, 0], (p @ wd - rest / (1 + rest) * wd[tc]) / n, (p - hot * rest / (1 + rest)).T @ hd / n]
+    top = rest / (1 + rest) * off / n  # of the targets' terms
+    terms = p / n * (1.1 * B + 4 * dz + _acc(v) + 64 * E)
+    bound = [(loss * off)[:, 0], terms @ wd.abs() + top * wd[tc].abs(),
+             (p / n * (2.2 * B + 4 * dz + _acc(n) + 64 * E) + hot * top * (1 + n * E)).T @ hd.abs()]
+    dtable = torch.empty((v, d), device="cuda")
+    got = ns.muon_head_loss_grad(h.cuda(), w.cuda(), tc, dtable=dtable, pieces=pieces)
+    only = ns.muon_head_loss(h.cuda(), w.cuda(), tc)
+    assert not (got[0] < 0).any() and not (only < 0).any()
+    _check((only,), want[:1], bound[:1])
+    _check(got, want, bound)
