@@ -105,6 +105,8 @@ int muon_layer_norm_grad(const void* dy, const void* x, int x_type, const void* 
  * The device error word is the first int of the workspace, as for muon_ns_ws
  * (muon_ns_read_error, muon_ns_check; waits bounded by
  * muon_ns_set_wait_budget); a call on no tokens or no vocabulary leaves it.
+ * Where a wait ran out, every result of the call is NaN as well: loss, dh and
+ * all of dW, accumulated or not.
  * ------------------------------------------------------------------------- */
 
 /* Workspace of muon_head_loss (grad = 0) or muon_head_loss_grad (grad != 0).

@@ -182,6 +182,15 @@ __global__ void __launch_bounds__(256)
   if (p < count) start_row(R, h, W, hc, p, static_cast<unsigned int>(R.sorted[p]));
 }
 
+// Fills 4-byte words with NaN, of fp32 and of bf16 alike, by all threads of the
+// grid.  A call whose waits ran out answers with nothing else: the error word
+// lies in a workspace that the caller may not hold.
+__device__ __forceinline__ void fill_nan(void* to, long long words) {
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < words; i += step)
+    static_cast<uint32_t*>(to)[i] = 0x7FFF7FFFu;
+}
+
 struct HeadFinish {
   const float2* stat;
   int halves;  // statistics a row
@@ -199,7 +208,12 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
   __shared__ float red[2][4];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  if (F.again && R.ctl[kCtlRedo] == 0) return;
+  if (F.again) {
+    const int4 ctl = *reinterpret_cast<const int4*>(R.ctl);
+    static_assert(kCtlErr == 0 && kCtlRedo == 3, "control words");
+    if (ctl.x != 0) fill_nan(F.loss, R.tokens);
+    if (ctl.x != 0 || ctl.w == 0) return;
+  }
   const int count = R.ctl[kCtlCount];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (long long p = blockIdx.x; p < R.tokens; p += gridDim.x) {
@@ -272,14 +286,24 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
 // a row and 256 of its columns.  With many items a warp takes one; with few
 // (SHARED), where splits are many, a CTA's warps share one, a contiguous part of
 // the splits each.
+// The gradient's last kernel: where a wait ran out, loss, dh and dW (dW_words
+// 4-byte words) become NaN.
 template <bool SHARED>
 __global__ void __launch_bounds__(256)
     head_join_dh(const HeadRows R, const float* __restrict__ part, const bf16* __restrict__ W, bf16* __restrict__ dh,
-                 int slices) {
+                 int slices, float* __restrict__ loss, void* __restrict__ dW, long long dW_words) {
   __shared__ float red[SHARED ? 8 : 1][256];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int count = R.ctl[kCtlCount], splits = R.ctl[kCtlSplits];
+  const int4 ctl = *reinterpret_cast<const int4*>(R.ctl);
+  static_assert(kCtlErr == 0 && kCtlCount == 1 && kCtlSplits == 2, "control words");
+  if (ctl.x != 0) {
+    fill_nan(loss, R.tokens);
+    fill_nan(dh, R.tokens * R.dim / 2);
+    fill_nan(dW, dW_words);
+    return;
+  }
+  const int count = ctl.y, splits = ctl.z;
   const long long rows = static_cast<long long>(token_pairs(count)) * kHeadRows;
   const long long items = R.tokens * slices;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -595,7 +619,8 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
   const bool shared = items <= 16LL * sm_count();
   MNS_TRY(mns::launch_pdl(shared ? head_join_dh<true> : head_join_dh<false>,
                           dim3(static_cast<unsigned>(shared ? items : (items + 7) / 8)), dim3(256), 0, C.stream, R,
-                          static_cast<const float*>(f32_at(L.part)), C.W, C.dh, slices));
+                          static_cast<const float*>(f32_at(L.part)), C.W, C.dh, slices, C.loss, C.dW,
+                          V * D / (C.dW_f32 ? 1 : 2)));
   return MUON_NS_OK;
 }
 

@@ -240,7 +240,9 @@ def muon_head_loss(h: torch.Tensor, table: torch.Tensor, targets: torch.Tensor, 
     """Cross entropy of softmax(h table^T) at `targets`, a loss a token (fp32
     of targets' shape), without keeping the logits.  h and table are bfloat16;
     targets int32 or int64.  Tokens whose target is ignore_index or outside
-    the table have loss 0."""
+    the table have loss 0.  If a wait on the device runs out
+    (set_wait_budget), every loss is NaN; a `workspace` of the caller's has the
+    reason (read_error, muon_ns_check)."""
     dev, bits, n, vocab, dim = _head_args(h, table, targets)
     loss = torch.empty(targets.shape, dtype=torch.float32, device=h.device)
     wp, wb, _keep = _workspace(workspace, dev, "muon_head_workspace_size", n, vocab, dim, 0, 0)
@@ -256,7 +258,8 @@ def muon_head_loss_grad(h: torch.Tensor, table: torch.Tensor, targets: torch.Ten
     in one call; dloss (fp32 of targets' shape) defaults to the mean's, 1 / the
     number of tokens with a loss.  dh is bfloat16; dtable bfloat16 unless a
     float32 `dtable` is given, to which `accumulate` adds.  `pieces` of the
-    vocabulary bound the workspace (0: pieces of about 4 GiB)."""
+    vocabulary bound the workspace (0: pieces of about 4 GiB).  If a wait on the
+    device runs out, all three are NaN throughout, as in muon_head_loss."""
     dev, bits, n, vocab, dim = _head_args(h, table, targets)
     dp = None
     if dloss is not None:

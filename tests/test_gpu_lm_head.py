@@ -330,3 +330,28 @@ def test_confident_tokens_of_dense_rows(n, v, d, level, pieces):
     assert not (got[0] < 0).any() and not (only < 0).any()
     _check((only,), want[:1], bound[:1])
     _check(got, want, bound)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [300, 4500])
+def test_a_call_that_gave_up_returns_no_numbers(n, dtype):
+    # Without a workspace of the caller's the error word is out of reach: a call
+    # whose waits ran out answers NaN throughout, and the next one is right.
+    v, d = 4000, 512
+    h, w, t = (x.cuda() for x in _inputs(n, v, d, 21))
+    start = torch.ones((v, d), dtype=dtype, device="cuda")
+    args = dict(accumulate=True) if dtype == torch.float32 else {}
+    ref = [x.clone() for x in ns.muon_head_loss_grad(h, w, t, dtable=start.clone(), **args)]
+    alone = ns.muon_head_loss(h, w, t)
+    ns.set_wait_budget(1)
+    try:
+        got = ns.muon_head_loss_grad(h, w, t, dtable=start.clone(), **args)
+        only = ns.muon_head_loss(h, w, t)
+        torch.cuda.synchronize()
+    finally:
+        ns.set_wait_budget(0)
+    for x in (*got, only):
+        assert torch.isnan(x).all()
+    got = ns.muon_head_loss_grad(h, w, t, dtable=start.clone(), **args)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    assert torch.equal(ns.muon_head_loss(h, w, t), alone)
