@@ -39,6 +39,13 @@ def _shaped(t, shape, name):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _int(n, name):
+    """n, refused if it does not fit a C int: ctypes would keep its low bits."""
+    if not -1 << 31 <= n < 1 << 31:
+        raise _lib.MuonNSError(_lib.ERR_INVALID_ARG, f"{name} {n}")
+    return n
+
+
 # The current stream's handle without a Stream object around it, where this
 # PyTorch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -96,6 +103,7 @@ def muon_embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, dtype
     if table.dim() != 2:
         raise ValueError(f"table must be [vocab][dim], got shape {tuple(table.shape)}")
     vocab, dim = table.shape
+    _int(dim, "dim")
     shape = (*ids.shape, dim)
     if out is None:
         out = torch.empty(shape, dtype=dtype or table.dtype, device=table.device)
@@ -112,7 +120,7 @@ def muon_embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, dtype
 
 
 def embed_grad_workspace_size(tokens: int, vocab: int, dim: int) -> int:
-    return _size("muon_embed_grad_workspace_size", int(tokens), int(vocab), int(dim))
+    return _size("muon_embed_grad_workspace_size", int(tokens), int(vocab), _int(int(dim), "dim"))
 
 
 def muon_embed_grad(dy: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float = 1.0,
@@ -126,7 +134,7 @@ def muon_embed_grad(dy: torch.Tensor, ids: torch.Tensor, vocab: int, scale: floa
     ib = _tensor(ids, "ids", _IDS, dev)
     if dy.dim() != ids.dim() + 1:
         raise ValueError("dy must have one more axis than ids")
-    dim = dy.shape[-1]
+    dim = _int(dy.shape[-1], "dim")
     _shaped(dy, (*ids.shape, dim), "dy")
     if dtable is None:
         if accumulate:
@@ -156,7 +164,7 @@ def muon_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | 
     shape = x.shape
     if not shape:
         raise ValueError("x must have an axis to normalise over")
-    dim = shape[-1]
+    dim = _int(shape[-1], "dim")
     _shaped(weight, (dim,), "weight")
     bp = None
     if bias is not None:
@@ -178,7 +186,7 @@ def muon_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | 
 
 
 def layer_norm_grad_workspace_size(rows: int, dim: int) -> int:
-    return _size("muon_layer_norm_grad_workspace_size", int(rows), int(dim))
+    return _size("muon_layer_norm_grad_workspace_size", int(rows), _int(int(dim), "dim"))
 
 
 def muon_layer_norm_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor,
@@ -195,7 +203,7 @@ def muon_layer_norm_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor
     shape = x.shape
     if not shape:
         raise ValueError("x must have an axis to normalise over")
-    dim, lead = shape[-1], shape[:-1]
+    dim, lead = _int(shape[-1], "dim"), shape[:-1]
     _shaped(dy, shape, "dy")
     _shaped(weight, (dim,), "weight")
     _tensor(mean, "mean", _F32, dev)
@@ -220,7 +228,8 @@ def muon_layer_norm_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor
 # -------------------------------------------------------------------- head --
 
 def head_workspace_size(tokens: int, vocab: int, dim: int, grad: bool = True, pieces: int = 0) -> int:
-    return _size("muon_head_workspace_size", int(tokens), int(vocab), int(dim), int(bool(grad)), int(pieces))
+    return _size("muon_head_workspace_size", int(tokens), int(vocab), _int(int(dim), "dim"), int(bool(grad)),
+                 _int(int(pieces), "pieces"))
 
 
 def _head_args(h, table, targets):
@@ -232,7 +241,7 @@ def _head_args(h, table, targets):
     if not shape or table.dim() != 2 or table.shape[1] != shape[-1]:
         raise ValueError(f"h and table must be [...][dim] and [vocab][dim], got {tuple(shape)} and {tuple(table.shape)}")
     _shaped(targets, shape[:-1], "targets")
-    return dev, bits, targets.numel(), table.shape[0], table.shape[1]
+    return dev, bits, targets.numel(), table.shape[0], _int(table.shape[1], "dim")
 
 
 def muon_head_loss(h: torch.Tensor, table: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
@@ -261,6 +270,7 @@ def muon_head_loss_grad(h: torch.Tensor, table: torch.Tensor, targets: torch.Ten
     vocabulary bound the workspace (0: pieces of about 4 GiB).  If a wait on the
     device runs out, all three are NaN throughout, as in muon_head_loss."""
     dev, bits, n, vocab, dim = _head_args(h, table, targets)
+    _int(pieces, "pieces")
     dp = None
     if dloss is not None:
         _tensor(dloss, "dloss", _F32, dev)

@@ -65,3 +65,19 @@ def test_head():
             (ValueError, lambda: g(h, w, t, workspace=torch.zeros(1 << 20, dtype=torch.uint8)))):
         with pytest.raises(error):
             call()
+
+
+def test_axes_past_an_int():
+    # 64 columns of 2^32 + 64, were a C int to keep the low bits: refused, not
+    # computed on the first columns.
+    n = (1 << 32) + 64
+    x = torch.empty((1, n), dtype=torch.bfloat16, device="cuda")
+    ids, m = _c(1, dtype=torch.int64), _c(1)
+    for f in (lambda: ns.muon_embed(x, ids), lambda: ns.muon_embed_grad(x, ids, 1, dtable=torch.empty_like(x)), lambda: ns.muon_layer_norm(x, x[0]),
+              lambda: ns.muon_layer_norm_grad(x, x, x[0], m, m), lambda: ns.muon_head_loss(x, x, ids),
+              lambda: ns.muon_head_loss_grad(x, x, ids)):
+        with pytest.raises(ns.MuonNSError):
+            f()
+    h = _c(2, 8, dtype=torch.bfloat16)
+    with pytest.raises(ns.MuonNSError):
+        ns.muon_head_loss_grad(h, h, _c(2, dtype=torch.int64), pieces=1 << 32)

@@ -199,3 +199,14 @@ def test_binding_refuses_host_tensors():
               lambda: ns.muon_head_loss_grad(x.bfloat16(), x.bfloat16(), ids)):
         with pytest.raises(TypeError):
             f()
+
+
+@pytest.mark.parametrize("size", [lambda d: ns.embed_grad_workspace_size(2000, 100, d), lambda d: ns.layer_norm_grad_workspace_size(50000, d),
+                                  lambda d: ns.head_workspace_size(1000, 500, d), lambda d: ns.head_workspace_size(1000, 500, 64, True, d)])
+def test_sizes_past_an_int_are_refused(size):
+    # A C int would keep the low 32 bits: 64 of 2^32 + 64.
+    for n in ((1 << 32) + 64, (1 << 31) + 64, -(1 << 32) + 64):
+        with pytest.raises(ns.MuonNSError) as e:
+            size(n)
+        assert e.value.status == BAD
+    assert size(64) > 0
