@@ -12,7 +12,7 @@
  *     status code of muon_ns.h is returned.  Workspaces are device memory,
  *     256-byte aligned, of at least the size the _workspace_size function
  *     gives; their contents need not be initialised and carry nothing from one
- *     call to the next.
+ *     call to the next.  Where that size is 0, the workspace is not looked at.
  *   - Element types are MUON_LM_BF16 or MUON_LM_F32.  Sums, norm statistics
  *     and softmax statistics are held in fp32 whatever the element type, and
  *     results are rounded once.

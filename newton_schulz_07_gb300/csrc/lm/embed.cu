@@ -842,8 +842,10 @@ int muon_embed_grad(const void* dy, int dy_type, const void* ids, int ids_bits, 
   if (tokens > 0 && overlap(dy, static_cast<size_t>(tokens) * dim * type_size(dy_type), dtable, table_bytes))
     return MUON_NS_ERR_INVALID_ARG;
   const SumLayout L = sum_layout(tokens, dim);
-  if (tokens > kFewTokens && (!workspace || workspace_bytes < L.total)) return MUON_NS_ERR_WORKSPACE;
-  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MUON_NS_ERR_ALIGNMENT;
+  if (tokens > kFewTokens) {
+    if (!workspace || workspace_bytes < L.total) return MUON_NS_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MUON_NS_ERR_ALIGNMENT;
+  }
   if ((s = muon_ns_device_supported(-1)) != MUON_NS_OK) return s;
   if (tokens == 0) return accumulate ? MUON_NS_OK : status_of(cudaMemsetAsync(dtable, 0, table_bytes, stream));
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -651,8 +651,10 @@ int muon_head_loss(const muon_bf16* h, const muon_bf16* W, long long tokens, lon
   if (!aligned(h, 16) || !aligned(W, 16) || !aligned(loss, 4) || !aligned(targets, target_bits / 8))
     return MUON_NS_ERR_ALIGNMENT;
   const HeadLayout L = head_layout(tokens, vocab, dim, false, 1);
-  if (vocab > 0 && (!workspace || workspace_bytes < L.total)) return MUON_NS_ERR_WORKSPACE;
-  if (!aligned(workspace, 256)) return MUON_NS_ERR_ALIGNMENT;
+  if (vocab > 0) {
+    if (!workspace || workspace_bytes < L.total) return MUON_NS_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return MUON_NS_ERR_ALIGNMENT;
+  }
   if ((s = muon_ns_device_supported(-1)) != MUON_NS_OK) return s;
   if (vocab == 0) return status_of(cudaMemsetAsync(loss, 0, sizeof(float) * tokens, stream));
   HeadCall C = {};
@@ -689,8 +691,10 @@ int muon_head_loss_grad(const muon_bf16* h, const muon_bf16* W, long long tokens
       overlap(dh, hb, dW, db))
     return MUON_NS_ERR_INVALID_ARG;
   const HeadLayout L = head_layout(tokens, vocab, dim, true, pieces);
-  if (tokens > 0 && vocab > 0 && (!workspace || workspace_bytes < L.total)) return MUON_NS_ERR_WORKSPACE;
-  if (!aligned(workspace, 256)) return MUON_NS_ERR_ALIGNMENT;
+  if (tokens > 0 && vocab > 0) {
+    if (!workspace || workspace_bytes < L.total) return MUON_NS_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return MUON_NS_ERR_ALIGNMENT;
+  }
   if ((s = muon_ns_device_supported(-1)) != MUON_NS_OK) return s;
   if (tokens == 0 || vocab == 0) {
     cudaError_t e = cudaSuccess;

@@ -449,8 +449,10 @@ int muon_layer_norm_grad(const void* dy, const void* x, int x_type, const void* 
     return MUON_NS_ERR_ALIGNMENT;
   size_t need = 0;
   muon_layer_norm_grad_workspace_size(rows, dim, &need);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return MUON_NS_ERR_WORKSPACE;
-  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MUON_NS_ERR_ALIGNMENT;
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return MUON_NS_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MUON_NS_ERR_ALIGNMENT;
+  }
   if ((s = muon_ns_device_supported(-1)) != MUON_NS_OK) return s;
   if (rows == 0) {  // sums over no rows
     cudaError_t e = cudaMemsetAsync(dweight, 0, sizeof(float) * dim, stream);

@@ -210,3 +210,15 @@ def test_sizes_past_an_int_are_refused(size):
             size(n)
         assert e.value.status == BAD
     assert size(64) > 0
+
+
+@pytest.mark.parametrize("call", [_embed_grad, _norm_grad, _head, _head_grad])
+def test_a_workspace_that_is_not_needed_is_not_looked_at(call):
+    # Past the checks of arguments: done, or the lack of a device.
+    few = {_embed_grad: dict(tokens=0, acc=1), _norm_grad: dict(rows=0, dim=0), _head: dict(n=0),
+           _head_grad: dict(n=0, v=0, dw=None)}[call]
+    for ws in (None, SP + 16):
+        assert call(ws=ws, wsb=16, **few) in (0, _lib.ERR_UNSUPPORTED_DEVICE)
+    if call in (_embed_grad, _norm_grad) and not torch.cuda.is_available():
+        few = dict(tokens=256) if call is _embed_grad else dict(rows=3)
+        assert call(ws=SP + 16, wsb=0, **few) == _lib.ERR_UNSUPPORTED_DEVICE
