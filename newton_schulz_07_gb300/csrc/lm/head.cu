@@ -263,13 +263,14 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
       }
       continue;
     }
-    if (tid == 0) F.loss[token] = et >= kLeastTarget ? log1pf(s / et) : logf(s + et) + (c - zt);
-    if (F.hs == nullptr) continue;
-    const float f = g / (s + et);
-    if (tid == 0) {
-      R.scale[p] = f;
-      R.coef[p] = -g * (s / (s + et));
+    const auto put_loss = [&] {
+      if (tid == 0) F.loss[token] = et >= kLeastTarget ? log1pf(s / et) : logf(s + et) + (c - zt);
+    };
+    if (F.hs == nullptr) {
+      put_loss();
+      continue;
     }
+    const float f = g / (s + et);
     // hs is the MMAs' bf16 operand: one more rounding, up to 2^-8, in each term of
     // dW but the targets', which are added in fp32.
     for (int col = tid * 8; col < R.dim; col += 1024) {
@@ -279,6 +280,11 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
       for (int j = 0; j < 8; ++j) o[j] = f * to_f32(x.v[j]);
       store_vec<bf16, 8>(F.hs + p * R.dim + col, o);
     }
+    if (tid == 0) {
+      R.scale[p] = f;
+      R.coef[p] = -g * (s / (s + et));
+    }
+    put_loss();
   }
 }
 
@@ -286,16 +292,25 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
 // a row and 256 of its columns.  With many items a warp takes one; with few
 // (SHARED), where splits are many, a CTA's warps share one, a contiguous part of
 // the splits each.
+//
 // The gradient's last kernel: where a wait ran out, loss, dh and dW (dW_words
 // 4-byte words) become NaN.
+// (5 CTAs an SM: with the registers that the filling would take of its own
+// accord, 3, 8192 x 2048 takes 47 us for 39.)
 template <bool SHARED>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, SHARED ? 4 : 5)
     head_join_dh(const HeadRows R, const float* __restrict__ part, const bf16* __restrict__ W, bf16* __restrict__ dh,
                  int slices, float* __restrict__ loss, void* __restrict__ dW, long long dW_words) {
   __shared__ float red[SHARED ? 8 : 1][256];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long i = SHARED ? blockIdx.x : static_cast<long long>(blockIdx.x) * 8 + warp;
+  const bool item = i < R.tokens * slices;
+  const long long p = item ? i / slices : 0;
   const int4 ctl = *reinterpret_cast<const int4*>(R.ctl);
+  // (Asked for before the control words are looked at.)
+  const unsigned int token = static_cast<unsigned int>(R.sorted[p]);
   static_assert(kCtlErr == 0 && kCtlCount == 1 && kCtlSplits == 2, "control words");
   if (ctl.x != 0) {
     fill_nan(loss, R.tokens);
@@ -303,10 +318,9 @@ __global__ void __launch_bounds__(256)
     fill_nan(dW, dW_words);
     return;
   }
+  if (!item) return;
   const int count = ctl.y, splits = ctl.z;
   const long long rows = static_cast<long long>(token_pairs(count)) * kHeadRows;
-  const long long items = R.tokens * slices;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto add = [&](long long p, int c, int s0, int s1, float (&o)[8]) {
 #pragma unroll 8
     for (int s = s0; s < s1; ++s) {
@@ -315,12 +329,8 @@ __global__ void __launch_bounds__(256)
       for (int j = 0; j < 8; ++j) o[j] += v.v[j];
     }
   };
-  const long long i = SHARED ? blockIdx.x : static_cast<long long>(blockIdx.x) * 8 + warp;
-  if (i >= items) return;
-  const long long p = i / slices;
   const int c = static_cast<int>(i - p * slices) * 256 + lane * 8;
   const bool live = p < count && c < R.dim;
-  const unsigned int token = static_cast<unsigned int>(R.sorted[p]);
   Vec<bf16, 8> w = {};
   float f = 0.0f, k = 0.0f;
   auto target = [&] {
