@@ -16,8 +16,12 @@
  *   - Element types are MUON_LM_BF16 or MUON_LM_F32.  Sums, norm statistics
  *     and softmax statistics are held in fp32 whatever the element type, and
  *     results are rounded once.
- *   - Every result is deterministic: no floating-point atomics, and each sum
- *     is taken in an order that the sizes alone determine.
+ *   - Results are deterministic: the same inputs at addresses of the same
+ *     alignment give the same bits, with no floating-point atomics.  The order
+ *     of a sum follows from the sizes and types, in the layer norm also from
+ *     the pointers' alignment (which sets the width of accesses), and in the
+ *     head from the targets (tokens are taken in their order, and how many have
+ *     a loss sets the splits of dh).
  */
 #ifndef MUON_LM_H
 #define MUON_LM_H
@@ -86,8 +90,10 @@ int muon_layer_norm_grad(const void* dy, const void* x, int x_type, const void* 
                          float* dbias, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
- * Output head: softmax cross entropy of h W^T over a large vocabulary, without
- * keeping the logits.  For token n with target t,
+ * Output head: softmax cross entropy of h W^T over a large vocabulary.  The
+ * logits are not kept: the losses alone hold none of them, the gradient holds
+ * bf16 probabilities of one piece of the vocabulary (`pieces` below) in the
+ * workspace.  For token n with target t,
  *   z = h_n W^T,  loss_n = log sum_v exp(z_v) - z_t,
  * and with g_n = dloss[n] (1 / (tokens with a loss) if dloss is NULL) and
  * p = softmax(z), the gradient of sum_n g_n loss_n is
@@ -100,8 +106,10 @@ int muon_layer_norm_grad(const void* dy, const void* x, int x_type, const void* 
  * dim must be a multiple of 8 (16-byte rows) and h, W, dh and dW 16-byte
  * aligned: MUON_NS_ERR_ALIGNMENT otherwise.  dh and dW overlap nothing.
  * Products accumulate in fp32 on the tensor cores; sums, logarithms and the
- * targets' terms are fp32.  The probabilities enter dh and dW as bf16 operands,
- * and h with its factor g / s enters dW as bf16.
+ * targets' terms are fp32: a target that holds nearly all of the probability
+ * has its loss and its terms to the relative accuracy of the logits' differences.
+ * The other probabilities enter dh and dW as bf16 operands, and h with its factor
+ * g / sum exp enters dW as bf16, so an fp32 dW is no more exact than that.
  * The device error word is the first int of the workspace, as for muon_ns_ws
  * (muon_ns_read_error, muon_ns_check; waits bounded by
  * muon_ns_set_wait_budget); a call on no tokens or no vocabulary leaves it.

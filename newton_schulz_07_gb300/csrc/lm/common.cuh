@@ -155,6 +155,10 @@ __device__ __forceinline__ void copy_wait() {
 
 constexpr long long kMaxRows = 1LL << 30;
 constexpr int kMaxDim = 1 << 20;
+// SMs of a GB300, for what is settled without a device to ask: workspace sizes,
+// the grids that fill them, and the head's splits.  Fewer SMs would take the same
+// grids in more turns.
+constexpr int kSms = 152;
 
 inline int type_size(int type) { return type == MUON_LM_F32 ? 4 : 2; }
 inline bool type_ok(int type) { return type == MUON_LM_BF16 || type == MUON_LM_F32; }

@@ -1,5 +1,6 @@
-// The output head's cross entropy and its gradient, without keeping the
-// logits.
+// The output head's cross entropy and its gradient.  No logits are kept: the
+// losses alone need none in memory, the gradient holds bf16 exponentials of one
+// piece of the vocabulary.
 //
 //   z = h W^T, loss_n = log sum_v exp z_nv - z_nt, p = softmax(z),
 //   dz_nv = g_n (p_nv - [v = t_n]), dh = dz W, dW = dz^T h.
@@ -54,7 +55,7 @@ constexpr float kTopSum = 1.8446744e19f;  // 2^64
 // Below it (only where the reference is the largest logit) the target's
 // exponential may have lost digits, or be zero.
 constexpr float kLeastTarget = 5.421011e-20f;  // 2^-64
-constexpr int kHeadPairs = 76;            // CTA pairs the splits are chosen for
+constexpr int kHeadPairs = kSms / 2;      // CTA pairs the splits are chosen for
 // Pair rows walked together: of e or W as many are read again as there are
 // bands.  (8 to 32 for the logits differ by half a percent at 8192 tokens.)
 constexpr int kHeadGroup = 8, kLogitsGroup = 16;
@@ -581,7 +582,7 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
     }
     F.again = again;
     // (The second pass mostly has nothing to do: CTAs that start at once.)
-    const long long most = 152 * (again ? 4 : 16);
+    const long long most = static_cast<long long>(sm_count()) * (again ? 4 : 16);
     const unsigned finish_grid = static_cast<unsigned>(N < most ? N : most);
     MNS_TRY(mns::launch_pdl(head_finish, dim3(finish_grid), dim3(128), 0, C.stream, R, F));
   }

@@ -1,7 +1,7 @@
 // Layer norm, per row: mu = mean(x), var = mean((x - mu)^2),
 // r = 1/sqrt(var + eps), y = (x - mu) r w + b.
 //
-// A group of G threads (a power of two, 32 to 1024) keeps its row in
+// A group of G threads (a power of two, 8 to 1024) keeps its row in
 // registers, kFwdPer elements a thread at most, so x is read once and the
 // variance is taken about the mean (no cancellation).  Bound by HBM traffic.
 // Many rows go through a grid that stays (the _ring kernel): while a row is

@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(FEW ? kFewCta : (G > kNormCta ? G : kNormCta))
 
 // The same with the rows of x and dy copied to shared memory one turn ahead
 // (cp.async; a thread copies and reads its own elements, so no barrier is
-// needed for them, except for those copied by words) and read from there twice, which leaves the registers to
-// kRingPer columns of dw and db a thread.
+// needed for them, except for those copied by words) and read from there twice,
+// which leaves the registers to kRingPer columns of dw and db a thread.
 template <typename T, typename TW, int VEC, int G>
 __global__ void __launch_bounds__(G > kNormCta ? G : kNormCta, G > kNormCta ? 1 : 2)
     layer_norm_bwd_ring(const T* dy, const T* x, const TW* __restrict__ w, const float* __restrict__ mean,
@@ -392,12 +392,11 @@ int few_ctas(long long rows, int dim) {
 // Partial rows of dw and db: CTAs of the backward kernel.  Two CTAs of 256
 // threads an SM, or one of more threads, but no more than there are rows.
 int bwd_parts(long long rows, int dim, int per_thread) {
-  const int sms = 152;
   if (dim > kBwdMax) return static_cast<int>(rows < 64 ? rows : 64);
   const int g = group_of(dim, per_thread);
   const long long per = g > kNormCta ? 1 : kNormCta / g;
   const long long need = (rows + per - 1) / per;
-  const long long most = static_cast<long long>(sms) * (g > kNormCta ? 1 : 2);
+  const long long most = static_cast<long long>(kSms) * (g > kNormCta ? 1 : 2);
   return static_cast<int>(need < most ? need : most);
 }
 

@@ -2,7 +2,10 @@
 
 As in ns.py, argument marshalling only; names follow the C entry points.
 Tensors are contiguous CUDA tensors of bfloat16 or float32 on one device, and
-work is enqueued on that device's current stream.  The small calls take about
+work is enqueued on that device's current stream.  The head's h and table are
+bfloat16, with a dim that is a multiple of 8.  As everywhere in this package,
+autograd is not involved: results require no gradient whatever the arguments
+do, and the backward pass is the caller's to call.  The small calls take about
 as long to issue as to run, so the checks here are kept to a few tests a
 tensor.
 """
@@ -247,7 +250,7 @@ def _head_args(h, table, targets):
 def muon_head_loss(h: torch.Tensor, table: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
                    workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Cross entropy of softmax(h table^T) at `targets`, a loss a token (fp32
-    of targets' shape), without keeping the logits.  h and table are bfloat16;
+    of targets' shape), without logits in memory.  h and table are bfloat16;
     targets int32 or int64.  Tokens whose target is ignore_index or outside
     the table have loss 0.  If a wait on the device runs out
     (set_wait_budget), every loss is NaN; a `workspace` of the caller's has the
@@ -266,8 +269,10 @@ def muon_head_loss_grad(h: torch.Tensor, table: torch.Tensor, targets: torch.Ten
     """(loss, dh, dtable): muon_head_loss and the gradient of sum(dloss * loss)
     in one call; dloss (fp32 of targets' shape) defaults to the mean's, 1 / the
     number of tokens with a loss.  dh is bfloat16; dtable bfloat16 unless a
-    float32 `dtable` is given, to which `accumulate` adds.  `pieces` of the
-    vocabulary bound the workspace (0: pieces of about 4 GiB).  If a wait on the
+    float32 `dtable` is given, to which `accumulate` adds (its products' operands
+    are bfloat16 all the same).  The workspace holds the bfloat16 probabilities
+    of one of `pieces` of the vocabulary (0: pieces of about 4 GiB; more than
+    one cost up to a third more work).  If a wait on the
     device runs out, all three are NaN throughout, as in muon_head_loss."""
     dev, bits, n, vocab, dim = _head_args(h, table, targets)
     _int(pieces, "pieces")
