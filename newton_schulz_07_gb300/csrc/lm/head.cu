@@ -183,14 +183,9 @@ __global__ void __launch_bounds__(256)
   if (p < count) start_row(R, h, W, hc, p, static_cast<unsigned int>(R.sorted[p]));
 }
 
-// Fills 4-byte words with NaN, of fp32 and of bf16 alike, by all threads of the
-// grid.  A call whose waits ran out answers with nothing else: the error word
-// lies in a workspace that the caller may not hold.
-__device__ __forceinline__ void fill_nan(void* to, long long words) {
-  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < words; i += step)
-    static_cast<uint32_t*>(to)[i] = 0x7FFF7FFFu;
-}
+// A call whose waits ran out answers with NaN alone: the error word lies in a
+// workspace that the caller may not hold.
+constexpr uint32_t kNanWord = 0x7FFF7FFFu;  // of fp32 and of bf16 alike
 
 struct HeadFinish {
   const float2* stat;
@@ -212,7 +207,9 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
   if (F.again) {
     const int4 ctl = *reinterpret_cast<const int4*>(R.ctl);
     static_assert(kCtlErr == 0 && kCtlRedo == 3, "control words");
-    if (ctl.x != 0) fill_nan(F.loss, R.tokens);
+    if (ctl.x != 0)
+      for (long long i = blockIdx.x * 128LL + threadIdx.x; i < R.tokens; i += gridDim.x * 128LL)
+        F.loss[i] = __uint_as_float(kNanWord);
     if (ctl.x != 0 || ctl.w == 0) return;
   }
   const int count = R.ctl[kCtlCount];
@@ -294,34 +291,30 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
 // (SHARED), where splits are many, a CTA's warps share one, a contiguous part of
 // the splits each.
 //
-// The gradient's last kernel: where a wait ran out, loss, dh and dW (dW_words
-// 4-byte words) become NaN.
-// (5 CTAs an SM: with the registers that the filling would take of its own
-// accord, 3, 8192 x 2048 takes 47 us for 39.)
+// The gradient's last kernel: where a wait ran out, dh becomes NaN here, and
+// loss and dW (dW_vecs 16-byte words) by one CTA more, which else does nothing.
+// (CTAs an SM: with 3 in place of 5, 8192 x 2048 takes 47 us for 39.)
 template <bool SHARED>
 __global__ void __launch_bounds__(256, SHARED ? 4 : 5)
     head_join_dh(const HeadRows R, const float* __restrict__ part, const bf16* __restrict__ W, bf16* __restrict__ dh,
-                 int slices, float* __restrict__ loss, void* __restrict__ dW, long long dW_words) {
+                 int slices, float* __restrict__ loss, uint4* __restrict__ dW, long long dW_vecs) {
   __shared__ float red[SHARED ? 8 : 1][256];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long i = SHARED ? blockIdx.x : static_cast<long long>(blockIdx.x) * 8 + warp;
-  const bool item = i < R.tokens * slices;
-  const long long p = item ? i / slices : 0;
   const int4 ctl = *reinterpret_cast<const int4*>(R.ctl);
-  // (Asked for before the control words are looked at.)
-  const unsigned int token = static_cast<unsigned int>(R.sorted[p]);
   static_assert(kCtlErr == 0 && kCtlCount == 1 && kCtlSplits == 2, "control words");
-  if (ctl.x != 0) {
-    fill_nan(loss, R.tokens);
-    fill_nan(dh, R.tokens * R.dim / 2);
-    fill_nan(dW, dW_words);
+  if (blockIdx.x == gridDim.x - 1) {
+    if (ctl.x == 0) return;
+#pragma unroll 1
+    for (long long i = threadIdx.x; i < R.tokens; i += 256) loss[i] = __uint_as_float(kNanWord);
+#pragma unroll 1
+    for (long long i = threadIdx.x; i < dW_vecs; i += 256) dW[i] = make_uint4(kNanWord, kNanWord, kNanWord, kNanWord);
     return;
   }
-  if (!item) return;
   const int count = ctl.y, splits = ctl.z;
   const long long rows = static_cast<long long>(token_pairs(count)) * kHeadRows;
+  const long long items = R.tokens * slices;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto add = [&](long long p, int c, int s0, int s1, float (&o)[8]) {
 #pragma unroll 8
     for (int s = s0; s < s1; ++s) {
@@ -330,8 +323,12 @@ __global__ void __launch_bounds__(256, SHARED ? 4 : 5)
       for (int j = 0; j < 8; ++j) o[j] += v.v[j];
     }
   };
+  const long long i = SHARED ? blockIdx.x : static_cast<long long>(blockIdx.x) * 8 + warp;
+  if (i >= items) return;
+  const long long p = i / slices;
   const int c = static_cast<int>(i - p * slices) * 256 + lane * 8;
   const bool live = p < count && c < R.dim;
+  const unsigned int token = static_cast<unsigned int>(R.sorted[p]);
   Vec<bf16, 8> w = {};
   float f = 0.0f, k = 0.0f;
   auto target = [&] {
@@ -358,10 +355,10 @@ __global__ void __launch_bounds__(256, SHARED ? 4 : 5)
   }
   if (c >= R.dim) return;
   if (!SHARED) target();
-  float out[8] = {};
-  if (live)
+  float out[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) out[j] = fmaf(f, o[j], k * to_f32(w.v[j]));
+  for (int j = 0; j < 8; ++j)
+    out[j] = ctl.x != 0 ? __uint_as_float(kNanWord) : live ? fmaf(f, o[j], k * to_f32(w.v[j])) : 0.0f;
   store_vec<bf16, 8>(dh + static_cast<long long>(token) * R.dim + c, out);
 }
 
@@ -629,9 +626,9 @@ int run_head(const HeadCall& C, const HeadLayout& L) {
   const long long items = N * slices;
   const bool shared = items <= 16LL * sm_count();
   MNS_TRY(mns::launch_pdl(shared ? head_join_dh<true> : head_join_dh<false>,
-                          dim3(static_cast<unsigned>(shared ? items : (items + 7) / 8)), dim3(256), 0, C.stream, R,
-                          static_cast<const float*>(f32_at(L.part)), C.W, C.dh, slices, C.loss, C.dW,
-                          V * D / (C.dW_f32 ? 1 : 2)));
+                          dim3(static_cast<unsigned>((shared ? items : (items + 7) / 8) + 1)), dim3(256), 0, C.stream, R,
+                          static_cast<const float*>(f32_at(L.part)), C.W, C.dh, slices, C.loss,
+                          static_cast<uint4*>(C.dW), V * D / (C.dW_f32 ? 4 : 8)));
   return MUON_NS_OK;
 }
 
