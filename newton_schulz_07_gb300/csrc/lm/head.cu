@@ -293,7 +293,8 @@ __global__ void __launch_bounds__(128) head_finish(const HeadRows R, const HeadF
 //
 // The gradient's last kernel: where a wait ran out, dh becomes NaN here, and
 // loss and dW (dW_vecs 16-byte words) by one CTA more, which else does nothing.
-// (CTAs an SM: with 3 in place of 5, 8192 x 2048 takes 47 us for 39.)
+// (CTAs an SM: with the registers of 3 in place of 5, 8192 x 2048 took 47 us for
+// 39, 36 in this form.)
 template <bool SHARED>
 __global__ void __launch_bounds__(256, SHARED ? 4 : 5)
     head_join_dh(const HeadRows R, const float* __restrict__ part, const bf16* __restrict__ W, bf16* __restrict__ dh,
