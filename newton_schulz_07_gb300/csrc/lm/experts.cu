@@ -46,7 +46,7 @@ bool map_rows(CUtensorMap (&map)[kExpBoxes], const void* base, bool f8, long lon
 }
 
 template <int MODE>
-cudaError_t launch_experts(const ExpertsGemm& P, long long units, cudaStream_t stream) {
+cudaError_t launch_experts(const ExpertsParam<MODE>& P, long long units, cudaStream_t stream) {
   constexpr int kSmem = ExpSmem<MODE>::kBytes;
   static std::atomic<int> resident[64];
   int dev = 0;
@@ -104,8 +104,9 @@ int check(long long rows, int experts, int out_dim, int dim, int step) {
   return MUON_NS_OK;
 }
 
-ExpertsGemm common(const int* offsets, long long rows, int experts, int* device_error) {
-  ExpertsGemm P = {};
+template <typename Param = ExpertsGemm>
+Param common(const int* offsets, long long rows, int experts, int* device_error) {
+  Param P = {};
   P.offsets = offsets;
   P.experts = experts;
   P.rows = static_cast<int>(rows);
@@ -173,7 +174,7 @@ int muon_experts_grad(const muon_bf16* dy, const muon_bf16* x, const muon_bf16* 
     if (e != cudaSuccess) return status_of(e);
   }
   if (!dW) return MUON_NS_OK;
-  ExpertsGemm P = common(offsets, rows, experts, device_error);
+  ExpertsGemmDw P = common<ExpertsGemmDw>(offsets, rows, experts, device_error);
   P.m = out_dim;
   P.n = dim;
   P.out = dW;
@@ -181,6 +182,9 @@ int muon_experts_grad(const muon_bf16* dy, const muon_bf16* x, const muon_bf16* 
   P.sectors = dim % 16 == 0 && aligned(dW, 32) ? 1 : 0;
   if (!map_bf16(&P.tmA, dy, out_dim, rows, 1, mns::kBlockK) || !map_bf16(&P.tmB[0], x, dim, rows, 1, mns::kBlockK))
     return MUON_NS_ERR_CUDA;
+  for (int i = 0; i < kExpTails; ++i)
+    if (!map_bf16(&P.tail[0][i], dy, out_dim, rows, 1, 1 << i) || !map_bf16(&P.tail[1][i], x, dim, rows, 1, 1 << i))
+      return MUON_NS_ERR_CUDA;
   const long long units = experts * tiles_of(out_dim) * tiles_of(dim);
   if (dW_type == MUON_LM_BF16) return status_of(launch_experts<kExpDwBf16>(P, units, stream));
   if (!map3d(&P.tmOut, dW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dim, out_dim, experts, 32, 32)) return MUON_NS_ERR_CUDA;

@@ -15,17 +15,21 @@
 // accumulator is y^T, so the epilogue transposes 32 x 32 pieces on their way
 // through shared memory (matrix-fragment TMEM loads, transposing matrix stores).
 //
-// dW's contraction runs over the expert's rows.  Its last 16 may hold rows of
-// others: they are zeroed in shared memory, in both operands, before the MMA
-// reads them.
+// dW's contraction runs over the expert's rows, and its last 16 may hold rows of
+// others, which have to be zero in both operands.  The copies see to it: a stage that
+// ends so is brought in boxes of 32 rows to one that hold the expert's rows alone,
+// and the rest of the 16 in boxes that start behind the last row of x, where a copy
+// reads zeros.  (Nothing but copies writes the stages, so the copies' own barrier
+// orders all of it for the MMA, in both CTAs.  Rows zeroed by a warp would have to
+// be handed from one CTA to the other with a release at cluster scope, about 2000
+// cycles.)
 //
 // Roles: warp 0 loads A by TMA (each CTA its 128 rows) into a ring of 6 stages
 // (kExp8: 3 of two k-blocks) and warp 3 its half of B (one thread that loaded both
 // took longer over a stage than its MMAs), warp 1 of the pair's first CTA issues MMAs into one of two TMEM
-// accumulators, warp 2 zeroes dW's rows, 8 more are the epilogue, two to a TMEM lane
-// quarter.  kExp8: warp 2 loads scales, and 16 are the epilogue.
-// The bytes of both CTAs are counted on the first one's barrier, but for the stages
-// that are zeroed: each CTA awaits its own and hands them on.  Waits are bounded;
+// accumulators, 8 more are the epilogue, two to a TMEM lane quarter.  kExp8: warp 2
+// loads scales, and 16 are the epilogue.
+// The bytes of both CTAs are counted on the first one's barrier.  Waits are bounded;
 // where one runs out the error word is set, the epilogue writes NaN in place of what
 // it has not got, copies and MMAs in flight are waited for and TMEM is freed.
 #pragma once
@@ -47,6 +51,7 @@ constexpr int kExpMax = 1024;      // experts
 constexpr int kExpBand = 16;       // row tiles of an expert that are walked together
 constexpr int kExpAhead = 16;      // units that a producer finds at once
 constexpr int kExpBoxes = 4;       // B boxes: of 128, 64, 32 or 16 rows
+constexpr int kExpTails = 6;       // dW's last rows: boxes of 1, 2, 4, 8, 16 or 32 of them
 constexpr long long kExpDrain = 4000000000LL;
 constexpr uint32_t kExpNan = 0x7FFF7FFFu;  // NaN of fp32 and of bf16 alike
 
@@ -96,6 +101,12 @@ struct ExpertsGemm {
   const float* xs;  // [rows][kblocks]
   const float* ws;  // [experts][ceil(m / 128)][kblocks]
 };
+// kExpDw*: the maps of the last rows of dy and x.
+struct ExpertsGemmDw : ExpertsGemm {
+  CUtensorMap tail[2][kExpTails];
+};
+template <int MODE>
+using ExpertsParam = std::conditional_t<ExpSmem<MODE>::kDw, ExpertsGemmDw, ExpertsGemm>;
 
 // One lane of the warp, the same at every call.
 __device__ __forceinline__ bool elect_one() {
@@ -129,15 +140,14 @@ __device__ __forceinline__ int2 expert_span(const int* offsets, int e, int rows)
 }
 
 // Arrival on the barrier of the pair's first CTA at this CTA's offset `bar` that
-// orders no memory: what it tells of has been completed by a wait or a fence.  (A
-// release at cluster scope costs about 2000 cycles, which a unit of dW cannot hide:
-// 65536 rows of 128 uneven experts took 492 us for 397.)
+// orders no memory: what it tells of, reads of TMEM, has been ordered by
+// tcgen05.wait::ld and tcgen05.fence.
 __device__ __forceinline__ void arrive_pair_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(ptx::mapa(bar, 0)) : "memory");
 }
 
 template <int MODE>
-__global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const __grid_constant__ ExpertsGemm P) {
+__global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const __grid_constant__ ExpertsParam<MODE> P) {
   using S = ExpSmem<MODE>;
   using EC = ElemCfg<false>;
   constexpr bool kDw = S::kDw;
@@ -146,15 +156,13 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
   constexpr int kK = MODE == kExp8 ? 128 : kBlockK;  // contraction of a k-block
   constexpr int kStages = S::kStages, kBufs = 2, kPer = S::kPer;
   extern __shared__ uint8_t smem_raw[];
-  // Barriers: filled[s], full[s], empty[s], tfull[b], tempty[b], mma_done, sfull[2], sempty[2].
-  __shared__ __align__(8) uint64_t bars[3 * kStages + 2 * kBufs + 5];
+  // Barriers: full[s], empty[s], tfull[b], tempty[b], mma_done, sfull[2], sempty[2].
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 2 * kBufs + 5];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
   // Stages this CTA has asked to be filled (with A, with B) and, in the pair's
-  // first CTA, the stages and accumulators its MMAs have committed; a bit a stage:
-  // how often it has been one to be zeroed, modulo 2.
+  // first CTA, the stages and accumulators its MMAs have committed.
   __shared__ int fills_sh[2], stages_sh, units_sh;
-  __shared__ uint32_t zeroed_sh;
   __shared__ int peer_abort_sh;  // the other CTA of the pair gave up
   // Units of the next turns of a producer and (kExp8, to spare registers) of the
   // epilogue's warps: expert, tiles, first row, rows.
@@ -168,12 +176,11 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
   int* err = P.err;
 
   const uint32_t bar0 = ptx::smem_u32(&bars[0]);
-  auto filled = [&](int s) { return bar0 + 8u * s; };
-  auto full = [&](int s) { return bar0 + 8u * (kStages + s); };
-  auto empty = [&](int s) { return bar0 + 8u * (2 * kStages + s); };
-  auto tfull = [&](int i) { return bar0 + 8u * (3 * kStages + i); };
-  auto tempty = [&](int i) { return bar0 + 8u * (3 * kStages + kBufs + i); };
-  const uint32_t mma_done = bar0 + 8u * (3 * kStages + 2 * kBufs);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
+  auto tfull = [&](int i) { return bar0 + 8u * (2 * kStages + i); };
+  auto tempty = [&](int i) { return bar0 + 8u * (2 * kStages + kBufs + i); };
+  const uint32_t mma_done = bar0 + 8u * (2 * kStages + 2 * kBufs);
   auto sfull = [&](int i) { return mma_done + 8u * (1 + i); };
   auto sempty = [&](int i) { return mma_done + 8u * (3 + i); };
   const uint32_t smem_base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -183,8 +190,7 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(filled(s), 1);
-      ptx::mbar_init(full(s), kDw ? 2 : 1);
+      ptx::mbar_init(full(s), 1);
       ptx::mbar_init(empty(s), 1);
     }
     for (int i = 0; i < kBufs; ++i) {
@@ -198,7 +204,6 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
     ptx::mbar_init(mma_done, 1);
     *abort_flag = 0;
     fills_sh[0] = fills_sh[1] = stages_sh = units_sh = peer_abort_sh = 0;
-    zeroed_sh = 0u;
     ptx::fence_barrier_init();
     ptx::prefetch_tensormap(&P.tmA);
     ptx::prefetch_tensormap(&P.tmB[0]);
@@ -343,6 +348,13 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
   // bytes do.)
   auto box_of = [&](const Unit& t) { return kDw || t.half > 64 ? 0 : t.half > 32 ? 1 : t.half > 16 ? 2 : 3; };
   auto b_bytes_of = [&](const Unit& t) { return 16384u >> box_of(t); };
+  // Bytes of A in k-block kb of a unit, and of B.  (Of a stage that ends in others'
+  // rows those of its last 16 and before.)
+  auto a_bytes = [&](const Unit& t, int kb) {
+    const int left = t.rows - kb * kK;
+    return kDw && others_rows(left) ? 256u * static_cast<uint32_t>((left + 15) & ~15) : static_cast<uint32_t>(kABytes);
+  };
+  auto b_bytes = [&](const Unit& t, int kb) { return kDw ? a_bytes(t, kb) : b_bytes_of(t); };
 
   const long long drain = P.budget > kExpDrain ? P.budget : kExpDrain;
   if (warp < S::kRoles) {
@@ -353,13 +365,12 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
       if (lane == 0) ptx::fence_proxy_async_global();
       int4* next = turns_sh[loads_a ? 0 : 1];
       int stage = 0, fills = 0;
-      uint32_t phase = 0, zeroed = 0u;
+      uint32_t phase = 0;
       bool ok = true;
       for (int turn = 0; turn < turns; ++turn) {
         look_ahead(turn, next);
         if (lane != 0 || !ok) continue;
         const Unit t = unit_of(next[turn % kExpAhead]);
-        const uint32_t bytes = kABytes + b_bytes_of(t);
         // Features or columns, or rows, that this CTA's part starts at.
         const int b_at = kDw ? t.J * kTileN + crank * (kTileN / 2) : t.row0 + crank * t.half;
         const int at = loads_a ? t.I * kTileM : b_at;
@@ -371,16 +382,37 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
           if (!ok) break;
           const uint32_t to = smem_base + stage * S::kStageBytes + (loads_a ? 0 : kPer * kABytes);
           const bool two = kPer == 2 && kb + 1 < t.kbs;
-          uint32_t fb = ptx::mapa(full(stage), 0);
-          if (kDw && others_rows(t.rows - kb * kK)) {
-            fb = ptx::mapa(filled(stage), static_cast<uint32_t>(crank));
-            zeroed ^= 1u << stage;
-            if (loads_a) ptx::mbar_arrive_expect_tx(filled(stage), bytes);
-          } else if (loads_a && leader) {
+          const uint32_t fb = ptx::mapa(full(stage), 0);
+          if (loads_a && leader) {
+            const uint32_t bytes = a_bytes(t, kb) + b_bytes(t, kb);
             ptx::mbar_arrive_expect_tx(full(stage), two ? 4 * bytes : 2 * bytes);
-            if (kDw) ptx::mbar_arrive(full(stage));  // in place of the two CTAs' handing on
           }
-          if (loads_a ? kAMn : kBMn) {
+          bool tail = false;
+          if constexpr (kDw) {
+            const int left = t.rows - kb * kK;
+            tail = others_rows(left);
+            if (tail) {
+              // Rows on from `row` of the stage, from row `from` of x or dy: the boxes of
+              // n rows' binary digits.  (A box may start at any row of the swizzle's
+              // pattern of 8, which goes by the shared-memory address.)
+              auto boxes = [&](int row, int n, int from, bool step) {
+#pragma unroll 1
+                for (int i = kExpTails - 1; i >= 0; --i) {
+                  if (!(n >> i & 1)) continue;
+#pragma unroll
+                  for (int c = 0; c < 2; ++c)
+                    ptx::tma_load_3d_pair(to + c * EC::kMnChunkBytes + row * 128, &P.tail[loads_a ? 0 : 1][i], fb,
+                                          at + c * EC::kMnChunk, from, 0);
+                  row += 1 << i;
+                  if (step) from += 1 << i;
+                }
+              };
+              boxes(0, left, k0, true);
+              boxes(left, -left & 15, P.rows, false);  // behind the last row: zeros
+            }
+          }
+          if (tail) {
+          } else if (loads_a ? kAMn : kBMn) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
               ptx::tma_load_3d_pair(to + c * EC::kMnChunkBytes, tm, fb, at + c * EC::kMnChunk, k0, z);
@@ -397,7 +429,6 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
       }
       if (lane == 0) {
         fills_sh[loads_a ? 0 : 1] = fills;
-        if (loads_a) zeroed_sh = zeroed;
         // The last release of each stage is awaited here, so that after a full
         // run no commit is on its way to this CTA's barriers when it leaves.
         for (int i = fills > kStages ? fills - kStages : 0; ok && i < fills; ++i)
@@ -483,36 +514,7 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
         }
       }
     } else if (warp == 2) {
-      if (kDw) {
-        // ----------------------------------------------------------- zeroing
-        // Rows of other experts in the last MMA's 16 of a unit.
-        int fills = 0;
-        uint32_t phases = 0u;
-        Ahead ahead;
-        for (int turn = 0; turn < turns; ++turn) {
-          const Unit t = unit_at(turn, ahead);
-          fills += t.kbs;
-          const int left = t.rows - (t.kbs - 1) * kK;
-          if (t.kbs == 0 || !others_rows(left)) continue;
-          const int stage = (fills - 1) % kStages;
-          if (!warp_await(filled(stage), (phases >> stage) & 1u)) break;
-          phases ^= 1u << stage;
-          // In the four chunks of 64 columns that A and B are held in (zeroing
-          // whole 128-byte rows, the swizzle does not matter).
-          const uint32_t chunk = smem_base + stage * S::kStageBytes + (lane >> 3) * EC::kMnChunkBytes + (lane & 7) * 16;
-          for (int r = left; r < ((left + 15) & ~15); ++r) ptx::st_shared_v4(chunk + r * 128, 0u, 0u, 0u, 0u);
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            // (The fence has made sure that the rows are zero in this CTA's shared
-            // memory, where its own tensor core reads them.)
-            if (leader)
-              ptx::mbar_arrive(full(stage));
-            else
-              arrive_pair_relaxed(full(stage));
-          }
-        }
-      } else if (MODE == kExp8) {
+      if (MODE == kExp8) {
         // ----------------------------------------------------------- scales
         // Of the tile's rows, times that of the CTA's 128 rows of W, 8 k-blocks
         // together: a row's are next to one another.  (A k-block at a time, and by
@@ -775,7 +777,7 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
     // out the loading threads may have asked for different numbers of fills.
     // Copies of a fill are counted on the first CTA's barrier, which expects those
     // of both CTAs once its own A is asked for; the first CTA stands in for what is
-    // missing.  Stages to be zeroed are counted by each CTA.
+    // missing.
     auto remote = [](const int* p, int rank) {
       int v;
       asm volatile("ld.shared::cluster.s32 %0, [%1];"
@@ -801,26 +803,15 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
       }
       const int s = i % kStages;
       const uint32_t n = kPer == 2 && 2 * (i - before_turn) + 1 < t.kbs ? 2 : 1;  // k-blocks of the fill
-      const uint32_t own = n * ((i < fills[0] ? kABytes : 0) + (i < fills[1] ? b_bytes_of(t) : 0));
-      const uint32_t peer = n * ((i < fills[2] ? kABytes : 0) + (i < fills[3] ? b_bytes_of(t) : 0));
-      const uint32_t bytes = n * (kABytes + b_bytes_of(t));
-      if (kDw && others_rows(t.rows - (i - before_turn) * kK)) {
-        if (own == 0) continue;
-        uint32_t parity = (zeroed_sh >> s) & 1u;
-        if (i < fills[0]) {
-          stand_in(ptx::mapa(filled(s), static_cast<uint32_t>(crank)), bytes - own);
-          parity ^= 1u;
-        } else {
-          ptx::mbar_arrive_expect_tx(filled(s), own);
-        }
-        detail::drain_wait<true>(filled(s), parity, drain);
-      } else if (leader) {
-        if (i < fills[0]) {
-          stand_in(ptx::mapa(full(s), 0), 2 * bytes - own - peer);
-        } else {
+      const int kb = kPer * (i - before_turn);
+      const uint32_t A = n * a_bytes(t, kb), B = n * b_bytes(t, kb);
+      const uint32_t own = (i < fills[0] ? A : 0) + (i < fills[1] ? B : 0);
+      const uint32_t peer = (i < fills[2] ? A : 0) + (i < fills[3] ? B : 0);
+      if (leader) {
+        if (i < fills[0])
+          stand_in(ptx::mapa(full(s), 0), 2 * (A + B) - own - peer);
+        else
           ptx::mbar_arrive_expect_tx(full(s), own + peer);
-          if (kDw) ptx::mbar_arrive(full(s));
-        }
         detail::drain_wait<true>(full(s), (i / kStages) & 1, drain);
       }
     }
