@@ -588,6 +588,9 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
         tphase ^= 1u;
       }
     };
+    // What the bulk stores add to or write over was written by other kernels' ordinary
+    // stores.
+    if (MODE == kExpDwF32 && lane == 0) ptx::fence_proxy_async_global();
     Ahead ahead;
     for (int turn = 0; turn < turns; ++turn) {
       if (MODE == kExp8) look_ahead(turn, turns_sh[MODE == kExp8 ? 2 + e : 0]);

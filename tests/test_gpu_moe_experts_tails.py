@@ -42,3 +42,20 @@ def test_tails_added_to_what_is_there():
     start = torch.randn(alone.shape, device="cuda")
     got = ns.muon_experts_grad(dy, x, W, offsets, dW=start.clone(), accumulate=True, need_dx=False)[1]
     assert torch.isfinite(alone).all() and torch.equal(got, start + alone)
+
+
+def test_added_right_behind_the_kernel_that_wrote_it():
+    # dW is written by ordinary stores of the kernel just before, and read back by
+    # ordinary loads of the one just behind.
+    counts = [33, 5, 0, 200]
+    x, W, dy, offsets = _inputs(counts, 264, 520, 5)
+    alone = ns.muon_experts_grad(dy, x, W, offsets, need_dx=False)[1]
+    dW = torch.empty_like(alone)
+    same = []
+    for i in range(50):
+        dW.fill_(i)
+        ns.muon_experts_grad(dy, x, W, offsets, dW=dW, accumulate=True, need_dx=False)
+        same.append((dW == alone + i).all())
+        ns.muon_experts_grad(dy, x, W, offsets, dW=dW, need_dx=False)
+        same.append((dW == alone).all())
+    assert torch.stack(same).all()
