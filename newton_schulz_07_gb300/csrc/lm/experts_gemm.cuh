@@ -81,7 +81,11 @@ struct ExpSmem {
   static constexpr int kUnitsAt = kSpanAt + (kDw ? 0 : 8 * kExpMax);        // int [experts + 1]: units before
   static constexpr int kScalesAt = kUnitsAt + (kDw ? 0 : 4 * kExpMax + 16);  // kExp8: float [2][kExpScales][kRows]
   static constexpr int kBytes = kScalesAt + (MODE == kExp8 ? 2 * kExpScales * kRows * 4 : 0) + 1024;
-  static_assert(kBytes + 1024 <= 232448, "shared memory");  // with the static part
+  // The static part: units of the next turns (lists of kExpAhead), barriers, words.
+  static constexpr int kTurnLists = MODE == kExp8 ? 2 + kEpi : 2;
+  static constexpr int kBars = 2 * kStages + 2 * 2 + 5;
+  static constexpr int kStatic = 16 * kTurnLists * kExpAhead + 8 * kBars + 64;
+  static_assert(kBytes + kStatic <= 232448, "shared memory");
 };
 
 struct ExpertsGemm {
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
   constexpr int kStages = S::kStages, kBufs = 2, kPer = S::kPer;
   extern __shared__ uint8_t smem_raw[];
   // Barriers: full[s], empty[s], tfull[b], tempty[b], mma_done, sfull[2], sempty[2].
-  __shared__ __align__(8) uint64_t bars[2 * kStages + 2 * kBufs + 5];
+  __shared__ __align__(8) uint64_t bars[S::kBars];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
   // Stages this CTA has asked to be filled (with A, with B) and, in the pair's
@@ -166,7 +170,7 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
   __shared__ int peer_abort_sh;  // the other CTA of the pair gave up
   // Units of the next turns of a producer and (kExp8, to spare registers) of the
   // epilogue's warps: expert, tiles, first row, rows.
-  __shared__ int4 turns_sh[MODE == kExp8 ? 2 + S::kEpi : 2][kExpAhead];
+  __shared__ int4 turns_sh[S::kTurnLists][kExpAhead];
 
   ptx::griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
