@@ -23,7 +23,8 @@
  *
  * 8-bit storage: values in e4m3 (largest 448) and fp32 scales; the value stood
  * for is the product of the two.  A block's scale is its largest magnitude
- * divided by 448, 1 if that is zero.  A block that holds a NaN or an infinity
+ * divided by 448 (by the quantiser rounded up where it is below the normal
+ * numbers), 1 if that magnitude is zero.  A block that holds a NaN or an infinity
  * has a scale of NaN, so that all of it stands for NaN.  Blocks at an edge are
  * shorter.
  */

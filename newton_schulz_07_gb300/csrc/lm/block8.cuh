@@ -102,10 +102,14 @@ __device__ __forceinline__ uint32_t lanes_max(float m) {
 }
 
 // Scale of a block whose largest magnitude has these bits: NaN where the block
-// holds a NaN or an infinity, 1 where it is all zero.
+// holds a NaN or an infinity, 1 where it is all zero.  A scale below the normal
+// numbers is rounded up: to nearest it could be a few steps too small for the
+// block's largest values, or 0, which makes NaN of its zeros.
 __device__ __forceinline__ float scale_of(uint32_t bits) {
   if (bits >= 0x7F800000u) return __uint_as_float(0x7FFFFFFFu);
-  return bits == 0u ? 1.0f : __uint_as_float(bits) / kTop8;
+  if (bits == 0u) return 1.0f;
+  const float top = __uint_as_float(bits), scale = top / kTop8;
+  return scale < 1.1754944e-38f ? __fdiv_ru(top, kTop8) : scale;
 }
 
 // e4m3 of a pair, the first in the low byte.
