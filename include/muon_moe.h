@@ -48,9 +48,9 @@ extern "C" {
  * dim and the pointers allow are used.
  * ------------------------------------------------------------------------- */
 
-/* residual may be NULL (s is then not written), s and rstd may be NULL (not
- * wanted).  s may be x or residual, and y may be x or residual, but s and y are
- * not the same. */
+/* residual may be NULL (s is then not written: it is x, which y may not be where the
+ * gradient is wanted), s and rstd may be NULL (not wanted).  s may be x or residual,
+ * and y may be x or residual, but s and y are not the same. */
 int muon_rms_norm(const void* x, int x_type, const void* residual, const void* weight, int w_type, long long rows,
                   int dim, float eps, void* s, void* y, float* rstd, cudaStream_t stream);
 

@@ -66,7 +66,9 @@ def muon_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
     """Root-mean-square norm over the last axis of x + residual.  Returns (y, s,
     rstd): y and the sum s (x itself without a residual) of x's shape and dtype,
     rstd fp32 of x's shape without its last axis.  weight: bfloat16 or float32.
-    `out` (y) and `total` (s) may each be x or the residual."""
+    `out` (y) and `total` (s) may each be x or the residual.  Written over x without
+    a residual, y leaves no s: it is None, and the gradient, which needs the s, is not
+    to be had."""
     dev, xt, wt, shape, dim, rp = _norm_args(x, weight, residual)
     out = _out(out, shape, x.dtype, x, "out")
     if rp is not None:
@@ -76,7 +78,9 @@ def muon_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
     rstd = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
     _call("muon_rms_norm", dev, x.data_ptr(), xt, rp, weight.data_ptr(), wt, rstd.numel(), dim, eps,
           None if rp is None else total.data_ptr(), out.data_ptr(), rstd.data_ptr())
-    return out, x if rp is None else total, rstd
+    if rp is None:
+        total = None if out.data_ptr() == x.data_ptr() and x.numel() else x
+    return out, total, rstd
 
 
 def muon_rms_norm8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
