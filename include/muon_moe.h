@@ -50,13 +50,14 @@ extern "C" {
 
 /* residual may be NULL (s is then not written: it is x, which y may not be where the
  * gradient is wanted), s and rstd may be NULL (not wanted).  s may be x or residual,
- * and y may be x or residual, but s and y are not the same. */
+ * and y may be x or residual, but s and y are not the same; otherwise outputs overlap
+ * nothing. */
 int muon_rms_norm(const void* x, int x_type, const void* residual, const void* weight, int w_type, long long rows,
                   int dim, float eps, void* s, void* y, float* rstd, cudaStream_t stream);
 
 /* y in 8 bits, not rounded to x_type before: y e4m3 [rows][dim], scales fp32
- * [rows][ceil(dim / 128)].  y overlaps neither x nor residual.  (r goes into the
- * scales, so the products s weight have to be within fp32.) */
+ * [rows][ceil(dim / 128)].  y and scales overlap nothing.  (r goes into the scales,
+ * so the products s weight have to be within fp32.) */
 int muon_rms_norm8(const void* x, int x_type, const void* residual, const void* weight, int w_type, long long rows,
                    int dim, float eps, void* s, void* y, float* scales, float* rstd, cudaStream_t stream);
 
@@ -67,7 +68,8 @@ int muon_rms_norm_grad_workspace_size(long long rows, int dim, size_t* bytes);
  * a = dy weight,
  *   ds = rstd (a - xh mean_row(a xh)) + dsum,  dweight = sum_rows dy xh:
  * ds is the gradient of x and of the residual alike.  dsum, the gradient that
- * reaches s past the norm, may be NULL (none).  ds may be dy, s or dsum. */
+ * reaches s past the norm, may be NULL (none).  ds may be dy, s or dsum; otherwise
+ * outputs and workspace overlap nothing. */
 int muon_rms_norm_grad(const void* dy, const void* s, int x_type, const void* weight, int w_type, const float* rstd,
                        const void* dsum, long long rows, int dim, void* ds, float* dweight, void* workspace,
                        size_t workspace_bytes, cudaStream_t stream);

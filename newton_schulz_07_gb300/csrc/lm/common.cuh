@@ -5,6 +5,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -183,6 +184,18 @@ inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + bn && y < x + an;
+}
+
+// An array of a call.  Null and empty ones overlap nothing.
+struct Span {
+  const void* p;
+  size_t n;
+};
+inline bool overlaps(Span a, std::initializer_list<Span> others) {
+  if (!a.p || a.n == 0) return false;
+  for (const Span& b : others)
+    if (b.p && b.n > 0 && overlap(a.p, a.n, b.p, b.n)) return true;
+  return false;
 }
 
 inline int status_of(cudaError_t e) {

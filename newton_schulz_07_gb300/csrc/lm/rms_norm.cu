@@ -198,6 +198,13 @@ int run_norm(const void* x, int x_type, const void* residual, const void* weight
   if (out8 ? overlap(y, qb, x, xb) : overlap(y, xb, x, xb) && y != x) return MUON_NS_ERR_INVALID_ARG;
   if (residual && (out8 ? overlap(y, qb, residual, xb) : overlap(y, xb, residual, xb) && y != residual))
     return MUON_NS_ERR_INVALID_ARG;
+  const size_t blocks = (static_cast<size_t>(dim) + kBlock8 - 1) / kBlock8;
+  const Span rows_x = {x, xb}, rows_a = {residual, xb}, rows_s = {residual ? s : nullptr, xb}, rows_y = {y, out8 ? qb : xb},
+             w = {weight, static_cast<size_t>(dim) * type_size(w_type)}, rs = {rstd, 4 * static_cast<size_t>(rows)},
+             sc = {out8 ? scales : nullptr, 4 * blocks * rows};
+  if (overlaps(w, {rows_s, rows_y, rs, sc}) || overlaps(rs, {rows_x, rows_a, rows_s, rows_y, sc}) ||
+      overlaps(sc, {rows_x, rows_a, rows_s, rows_y}))
+    return MUON_NS_ERR_INVALID_ARG;
   if ((st = muon_ns_device_supported(-1)) != MUON_NS_OK) return st;
   return with_type(x_type, [&](auto xt) {
     return with_type(w_type, [&](auto wt) {

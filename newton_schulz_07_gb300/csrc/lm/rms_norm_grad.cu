@@ -327,6 +327,11 @@ int muon_rms_norm_grad(const void* dy, const void* s, int x_type, const void* we
     if (!workspace || workspace_bytes < need) return MUON_NS_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MUON_NS_ERR_ALIGNMENT;
   }
+  const Span g = {dy, bytes}, v = {s, bytes}, past = {dsum, bytes}, o = {rows > 0 ? ds : nullptr, bytes},
+             w = {weight, static_cast<size_t>(dim) * type_size(w_type)}, rs = {rstd, 4 * static_cast<size_t>(rows)},
+             dw = {dweight, 4 * static_cast<size_t>(dim)}, ws = {workspace, need};
+  if (overlaps(w, {o, dw, ws}) || overlaps(rs, {o, dw, ws}) || overlaps(dw, {g, v, past, o, ws}) || overlaps(ws, {g, v, past, o}))
+    return MUON_NS_ERR_INVALID_ARG;
   if ((st = muon_ns_device_supported(-1)) != MUON_NS_OK) return st;
   if (rows == 0) return status_of(cudaMemsetAsync(dweight, 0, sizeof(float) * dim, stream));  // a sum over no rows
   float* part = static_cast<float*>(workspace);

@@ -1,0 +1,38 @@
+"""Outputs that lie over other arrays of the same call are refused before a device is
+touched."""
+import pytest
+
+from newton_schulz_07_gb300 import _lib
+from test_moe_abi import _caller
+
+BAD, ALIGN = _lib.ERR_INVALID_ARG, _lib.ERR_ALIGNMENT
+A, B, C, D, E, F, G, H = (i << 32 for i in range(1, 9))
+
+_norm = _caller("muon_rms_norm", x=A, xt=0, res=B, w=C, wt=1, rows=50, d=24, eps=1e-6, s=D, y=E, rstd=F)
+_norm8 = _caller("muon_rms_norm8", x=A, xt=0, res=B, w=C, wt=1, rows=50, d=24, eps=1e-6, s=D, y=E, sc=G, rstd=F)
+_norm_grad = _caller("muon_rms_norm_grad", dy=A, s=B, xt=0, w=C, wt=1, rstd=D, dsum=E, rows=40000, d=24, ds=F, dw=G, ws=H, wsb=1 << 20)
+
+
+@pytest.mark.parametrize("call", [_norm, _norm8])
+@pytest.mark.parametrize("kw", [dict(s=C), dict(y=C), dict(y=C - 16), dict(rstd=C), dict(rstd=A), dict(rstd=B + 4), dict(rstd=D), dict(rstd=E)])
+def test_norm(call, kw):
+    assert call(**kw) == BAD
+
+
+def test_norm8():
+    for kw in (dict(sc=A), dict(sc=B), dict(sc=C + 4), dict(sc=D), dict(sc=E + 8), dict(sc=F), dict(y=D), dict(rstd=G + 196)):
+        assert _norm8(**kw) == BAD, kw
+    assert _norm8(sc=F + 200) not in (BAD, ALIGN)  # right behind the last of 50
+
+
+@pytest.mark.parametrize("kw", [
+    dict(ds=C), dict(ds=D), dict(ds=G), dict(ds=H), dict(dw=A), dict(dw=B), dict(dw=C), dict(dw=D + 4), dict(dw=E + 8), dict(dw=F),
+    dict(dw=H), dict(ws=A), dict(ws=B), dict(ws=C), dict(ws=D + 256), dict(ws=E), dict(ws=F), dict(ws=G)])
+def test_norm_grad(kw):
+    assert _norm_grad(**kw) == BAD
+
+
+def test_arrays_that_are_not_looked_at():
+    # Without a residual s is not written; few rows need no workspace.
+    for call, kw in ((_norm, dict(res=None, s=E)), (_norm, dict(res=None, s=C)), (_norm_grad, dict(rows=3, ws=A)), (_norm, dict(rstd=None))):
+        assert call(**kw) not in (BAD, ALIGN), kw
