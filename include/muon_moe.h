@@ -78,7 +78,7 @@ int muon_rms_norm_grad(const void* dy, const void* s, int x_type, const void* we
  * scales fp32 [batch][rows][ceil(dim / 128)].  square = 1: one for each block of
  * 128 rows and 128 columns of each of the batch's matrices, fp32
  * [batch][ceil(rows / 128)][ceil(dim / 128)], as muon_experts8 takes W.
- *   x  [batch][rows][dim] of x_type, q  e4m3 of the same shape; no overlap.
+ *   x  [batch][rows][dim] of x_type, q  e4m3 of the same shape; no overlap of any.
  * Limits: batch <= 65535, rows <= 2^30, dim <= 2^20. */
 int muon_quantize8(const void* x, int x_type, long long batch, long long rows, int dim, int square, void* q,
                    float* scales, cudaStream_t stream);

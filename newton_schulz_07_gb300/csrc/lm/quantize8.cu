@@ -84,7 +84,9 @@ extern "C" int muon_quantize8(const void* x, int x_type, long long batch, long l
   if (!x || !q || !scales) return MUON_NS_ERR_INVALID_ARG;
   if (!element_aligned(x, x_type) || !element_aligned(scales, MUON_LM_F32)) return MUON_NS_ERR_ALIGNMENT;
   const size_t n = static_cast<size_t>(batch) * rows * dim;
-  if (overlap(q, n, x, n * type_size(x_type))) return MUON_NS_ERR_INVALID_ARG;
+  const size_t lines = static_cast<size_t>(batch) * (square ? (rows + kBlock8 - 1) / kBlock8 : rows);
+  const Span in = {x, n * type_size(x_type)}, sc = {scales, 4 * lines * ((static_cast<size_t>(dim) + kBlock8 - 1) / kBlock8)};
+  if (overlaps({q, n}, {in, sc}) || overlaps(in, {sc})) return MUON_NS_ERR_INVALID_ARG;
   const int st = muon_ns_device_supported(-1);
   if (st != MUON_NS_OK) return st;
   // Single rows are one matrix whatever the stack.

@@ -36,3 +36,14 @@ def test_arrays_that_are_not_looked_at():
     # Without a residual s is not written; few rows need no workspace.
     for call, kw in ((_norm, dict(res=None, s=E)), (_norm, dict(res=None, s=C)), (_norm_grad, dict(rows=3, ws=A)), (_norm, dict(rstd=None))):
         assert call(**kw) not in (BAD, ALIGN), kw
+
+
+_quantize = _caller("muon_quantize8", x=A, xt=0, batch=2, rows=300, d=264, square=0, q=B, sc=C)
+
+
+def test_quantize():
+    for kw in (dict(sc=A), dict(sc=A + 2 * 2 * 300 * 264 - 4), dict(sc=B), dict(sc=B - 4 * 2 * 300 * 3 + 4)):
+        assert _quantize(**kw) == BAD, kw
+    for kw in (dict(sc=A + 2 * 2 * 300 * 264), dict(sc=B - 4 * 2 * 300 * 3), dict(sc=B - 4 * 2 * 3 * 3, square=1)):
+        assert _quantize(**kw) not in (BAD, ALIGN), kw
+    assert _quantize(sc=B - 4 * 2 * 3 * 3 + 4, square=1) == BAD
