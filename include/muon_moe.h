@@ -148,7 +148,8 @@ int muon_combine_grad(const void* dout, const void* y, int type, const int* slot
  * Limits: rows <= 2^30, experts <= 1024, out_dim, dim <= 2^20, fewer than 2^30
  * tiles of 256 x 256; out_dim and dim multiples of 8 (for muon_experts8 dim a
  * multiple of 16) and arrays 16-byte aligned: MUON_NS_ERR_ALIGNMENT otherwise.
- * Outputs overlap nothing.  Products accumulate in fp32 on the tensor cores.
+ * Outputs (`device_error` among them) overlap nothing.  Products accumulate in fp32 on
+ * the tensor cores.
  * `device_error` is an optional device int32 (may be NULL), as in muon_ns_gram:
  * MUON_NS_DEVERR_WAIT_TIMEOUT is set in it if a bounded wait runs out
  * (muon_ns_set_wait_budget), and nothing is where none does.  What such a call

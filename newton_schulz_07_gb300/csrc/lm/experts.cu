@@ -104,6 +104,8 @@ int check(long long rows, int experts, int out_dim, int dim, int step) {
   return MUON_NS_OK;
 }
 
+Span offsets_of(const int* offsets, int experts) { return {offsets, 4 * (static_cast<size_t>(experts) + 1)}; }
+
 template <typename Param = ExpertsGemm>
 Param common(const int* offsets, long long rows, int experts, int* device_error) {
   Param P = {};
@@ -134,7 +136,8 @@ int muon_experts(const muon_bf16* x, const muon_bf16* W, const int* offsets, lon
     return MUON_NS_ERR_ALIGNMENT;
   const size_t xb = 2 * static_cast<size_t>(rows) * dim, yb = 2 * static_cast<size_t>(rows) * out_dim;
   const size_t wb = 2 * static_cast<size_t>(experts) * out_dim * dim;
-  if (overlap(y, yb, x, xb) || overlap(y, yb, W, wb)) return MUON_NS_ERR_INVALID_ARG;
+  const Span rx = {x, xb}, ry = {y, yb}, w = {W, wb}, at = offsets_of(offsets, experts), word = {device_error, 4};
+  if (overlaps(ry, {rx, w, at, word}) || overlaps(word, {rx, w, at})) return MUON_NS_ERR_INVALID_ARG;
   if ((s = muon_ns_device_supported(-1)) != MUON_NS_OK) return s;
   ExpertsGemm P = common(offsets, rows, experts, device_error);
   P.m = out_dim;
@@ -157,9 +160,10 @@ int muon_experts_grad(const muon_bf16* dy, const muon_bf16* x, const muon_bf16* 
     return MUON_NS_ERR_ALIGNMENT;
   const size_t gb = 2 * static_cast<size_t>(rows) * out_dim, xb = 2 * static_cast<size_t>(rows) * dim;
   const size_t n = static_cast<size_t>(experts) * out_dim * dim, db = n * type_size(dW_type);
-  if (dx && (overlap(dx, xb, dy, gb) || overlap(dx, xb, x, xb) || overlap(dx, xb, W, 2 * n) || overlap(dx, xb, dW, dW ? db : 0)))
+  const Span rg = {dy, gb}, rx = {x, xb}, w = {W, 2 * n}, rdx = {dx, xb}, rdw = {dW, db}, at = offsets_of(offsets, experts),
+             word = {device_error, 4};
+  if (overlaps(rdx, {rg, rx, w, rdw, at, word}) || overlaps(rdw, {rg, rx, w, at, word}) || overlaps(word, {rg, rx, w, at}))
     return MUON_NS_ERR_INVALID_ARG;
-  if (dW && (overlap(dW, db, dy, gb) || overlap(dW, db, x, xb) || overlap(dW, db, W, 2 * n))) return MUON_NS_ERR_INVALID_ARG;
   if ((s = muon_ns_device_supported(-1)) != MUON_NS_OK) return s;
   if (rows == 0)
     return dW && !accumulate ? status_of(cudaMemsetAsync(dW, 0, db, stream)) : MUON_NS_OK;
@@ -203,9 +207,9 @@ int muon_experts8(const void* x, const float* x_scales, const void* W, const flo
     return MUON_NS_ERR_ALIGNMENT;
   const size_t xb = static_cast<size_t>(rows) * dim, yb = 2 * static_cast<size_t>(rows) * out_dim;
   const size_t kb = (static_cast<size_t>(dim) + 127) / 128, mb = (static_cast<size_t>(out_dim) + 127) / 128;
-  if (overlap(y, yb, x, xb) || overlap(y, yb, W, static_cast<size_t>(experts) * out_dim * dim) ||
-      overlap(y, yb, x_scales, 4 * kb * rows) || overlap(y, yb, W_scales, 4 * kb * mb * experts))
-    return MUON_NS_ERR_INVALID_ARG;
+  const Span rx = {x, xb}, ry = {y, yb}, w = {W, static_cast<size_t>(experts) * out_dim * dim}, xs = {x_scales, 4 * kb * rows},
+             ws = {W_scales, 4 * kb * mb * experts}, at = offsets_of(offsets, experts), word = {device_error, 4};
+  if (overlaps(ry, {rx, w, xs, ws, at, word}) || overlaps(word, {rx, w, xs, ws, at})) return MUON_NS_ERR_INVALID_ARG;
   if ((s = muon_ns_device_supported(-1)) != MUON_NS_OK) return s;
   ExpertsGemm P = common(offsets, rows, experts, device_error);
   P.m = out_dim;

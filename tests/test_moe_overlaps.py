@@ -47,3 +47,29 @@ def test_quantize():
     for kw in (dict(sc=A + 2 * 2 * 300 * 264), dict(sc=B - 4 * 2 * 300 * 3), dict(sc=B - 4 * 2 * 3 * 3, square=1)):
         assert _quantize(**kw) not in (BAD, ALIGN), kw
     assert _quantize(sc=B - 4 * 2 * 3 * 3 + 4, square=1) == BAD
+
+
+_experts = _caller("muon_experts", x=A, W=B, off=C, rows=50, e=3, o=16, d=24, y=D, err=E)
+_experts_grad = _caller("muon_experts_grad", dy=A, x=B, W=C, off=D, rows=50, e=3, o=16, d=24, dx=E, dW=F, wt=1, acc=0, err=G)
+_experts8 = _caller("muon_experts8", x=A, xs=B, W=C, Ws=D, off=E, rows=50, e=3, o=16, d=32, y=F, err=G)
+
+
+def test_experts():
+    for kw in (dict(y=C), dict(y=C - 2 * 50 * 16 + 16), dict(y=E), dict(err=A + 4), dict(err=B), dict(err=C + 12), dict(err=D + 2 * 50 * 16 - 4)):
+        assert _experts(**kw) == BAD, kw
+    for kw in (dict(err=C + 16), dict(err=D + 2 * 50 * 16), dict(err=None), dict(y=C + 16)):
+        assert _experts(**kw) not in (BAD, ALIGN), kw
+
+
+def test_experts_grad():
+    for kw in (dict(dx=D), dict(dW=D), dict(dx=G), dict(dW=G), dict(err=A), dict(err=B + 8), dict(err=C), dict(err=D + 12), dict(err=E), dict(err=F)):
+        assert _experts_grad(**kw) == BAD, kw
+    for kw in (dict(dx=None, err=E), dict(dW=None, err=F), dict(err=D + 16)):
+        assert _experts_grad(**kw) not in (BAD, ALIGN), kw
+
+
+def test_experts8():
+    for kw in (dict(y=E), dict(y=G), dict(err=A), dict(err=B + 196), dict(err=C), dict(err=D + 8), dict(err=E), dict(err=F)):
+        assert _experts8(**kw) == BAD, kw
+    for kw in (dict(err=B + 200), dict(err=D + 12)):
+        assert _experts8(**kw) not in (BAD, ALIGN), kw
