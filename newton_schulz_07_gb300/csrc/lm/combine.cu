@@ -199,7 +199,7 @@ int muon_combine_grad(const void* dout, const void* y, int type, const int* slot
   if (dy && (overlap(dy, yb, dout, ob) || (dgates && y && overlap(dy, yb, y, yb)) || overlap(dy, yb, slots, sb) ||
              (gates && overlap(dy, yb, gates, sb)) || (dgates && overlap(dy, yb, dgates, sb))))
     return MUON_NS_ERR_INVALID_ARG;
-  if (dgates && (overlap(dgates, sb, slots, sb) || (gates && overlap(dgates, sb, gates, sb)))) return MUON_NS_ERR_INVALID_ARG;
+  if (overlaps({dgates, sb}, {{slots, sb}, {gates, sb}, {dout, ob}, {y, yb}})) return MUON_NS_ERR_INVALID_ARG;
   if ((st = muon_ns_device_supported(-1)) != MUON_NS_OK) return st;
   const Combine C = {slots, gates, tokens, rows, k, dim};
   return with_type(type, [&](auto tt) {

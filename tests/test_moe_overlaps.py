@@ -73,3 +73,14 @@ def test_experts8():
         assert _experts8(**kw) == BAD, kw
     for kw in (dict(err=B + 200), dict(err=D + 12)):
         assert _experts8(**kw) not in (BAD, ALIGN), kw
+
+
+_combine_grad = _caller("muon_combine_grad", dout=A, y=B, yt=0, s=C, g=D, n=50, k=2, rows=900, d=24, dy=E, dg=F)
+
+
+def test_combine_grad():
+    for kw in (dict(dg=A), dict(dg=A + 2 * 50 * 24 - 4), dict(dg=B + 8), dict(dg=B + 2 * 900 * 24 - 4)):
+        assert _combine_grad(**kw) == BAD, kw
+        assert _combine_grad(**kw, dy=None) == BAD, kw
+    for kw in (dict(dg=A + 2 * 50 * 24), dict(dg=B + 2 * 900 * 24)):
+        assert _combine_grad(**kw) not in (BAD, ALIGN), kw
