@@ -290,6 +290,12 @@ __global__ void __launch_bounds__(512) route_place(const Route R) {
 // choice j is g_j (dg_j - inner), and elsewhere -p inner, p the softmax over all
 // experts; 0 where the gates are renormalised.
 //
+// Where one gate is nearly 1, inner is nearly its dg, and what is left of the
+// difference would be rounding.  So at the choices, with m that of the largest gate,
+// d_j = dg_j - dg_m and `rest` the sum of p elsewhere,
+//   dz_j = g_j (d_j - sum_i g_i d_i + dg_m rest):
+// at m the first term is 0 and what remains are the small terms themselves.
+//
 // Over all experts a warp takes a token (J logits a lane).
 template <typename T, int J>
 __global__ void __launch_bounds__(256)
@@ -312,23 +318,35 @@ __global__ void __launch_bounds__(256)
     for (int j = 1; j < J; ++j) top = fmaxf(top, p[j]);
     top = warp_max(top);
     const float own = e >= 0 ? expf(c - top) : 0.0f;
-    float sum = 0.0f;
+    uint32_t mine = 0u;  // of this lane's experts those that are choices
+    for (int i = 0; i < k; ++i) {
+      const int of = __shfl_sync(0xFFFFFFFFu, e, i);
+      if (of >= 0 && (of & 31) == lane) mine |= 1u << (of >> 5);
+    }
+    float sum = 0.0f, rest = 0.0f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       // (A token without any expert to be had has no gradient.)
       p[j] = lane + 32 * j < experts && top != -INFINITY ? expf(p[j] - top) : 0.0f;
       sum += p[j];
+      if (!(mine >> j & 1u)) rest += p[j];
     }
     sum = warp_sum(sum);
+    rest = warp_sum(rest);
     const float g = e >= 0 ? own / sum : 0.0f;
     const float inner = warp_sum(e >= 0 ? dg * g : 0.0f);
+    const float most = warp_max(c);
+    const uint32_t at_top = __ballot_sync(0xFFFFFFFFu, e >= 0 && c == most);
+    const float ref = __shfl_sync(0xFFFFFFFFu, dg, at_top != 0u ? __ffs(at_top) - 1 : 0);
+    const float d = e >= 0 ? dg - ref : 0.0f;
+    const float left = warp_sum(d * g);
     const float factor = sum == 0.0f ? 0.0f : -inner / sum;
     T* out = dlogits + t * experts;
 #pragma unroll
     for (int j = 0; j < J; ++j)
       if (lane + 32 * j < experts) out[lane + 32 * j] = from_f32<T>(p[j] * factor);
     __syncwarp();  // the choices' places are written again, by other lanes
-    if (e >= 0) out[e] = from_f32<T>(g * (dg - inner));
+    if (e >= 0) out[e] = from_f32<T>(g * (d - left + ref * (rest / sum)));
   }
 }
 
@@ -365,9 +383,13 @@ __global__ void __launch_bounds__(256)
   };
   const float sum = total(own);
   const float g = e >= 0 ? own / sum : 0.0f;
-  const float inner = total(e >= 0 ? dg * g : 0.0f);
+  const uint32_t group = (G == 32 ? 0xFFFFFFFFu : (1u << (G & 31)) - 1u) << (lane & ~(G - 1));
+  const uint32_t at_top = __ballot_sync(0xFFFFFFFFu, e >= 0 && c == top) & group;
+  const float ref = __shfl_sync(0xFFFFFFFFu, dg, at_top != 0u ? __ffs(at_top) - 1 : lane);
+  const float d = e >= 0 ? dg - ref : 0.0f;
+  const float left = total(d * g);
   __syncwarp();  // the choices' places are written again, by other lanes
-  if (e >= 0) dlogits[t * experts + e] = from_f32<T>(g * (dg - inner));
+  if (e >= 0) dlogits[t * experts + e] = from_f32<T>(g * (d - left));
 }
 
 template <typename F>
