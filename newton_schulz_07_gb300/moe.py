@@ -277,16 +277,18 @@ def muon_experts(x: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, out: t
     return out
 
 
-def muon_experts_grad(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor,
+def muon_experts_grad(dy: torch.Tensor, x: torch.Tensor | None, W: torch.Tensor, offsets: torch.Tensor,
                       dx: torch.Tensor | None = None, dW: torch.Tensor | None = None, accumulate: bool = False,
                       need_dx: bool = True, need_dW: bool = True, error: torch.Tensor | None = None):
     """Gradients of muon_experts: (dx, dW), dx bfloat16 (rows of no expert not
     written), dW float32 unless a bfloat16 `dW` is given, zero for an expert
     without rows; with `accumulate` it is added to a float32 dW.  need_dx or
-    need_dW False: that one is not computed, and None."""
+    need_dW False: that one is not computed, and None; x is read for dW alone and may
+    be None without it."""
     dev, n, e, o, d = _experts_args(dy, "dy", W, offsets, _BF16, 1)
-    _tensor(x, "x", _BF16, dev)
-    _shaped(x, (n, d), "x")
+    if x is not None or need_dW:
+        _tensor(x, "x", _BF16, dev)
+        _shaped(x, (n, d), "x")
     dx = _out(dx, (n, d), torch.bfloat16, dy, "dx") if need_dx else None
     wt = 1
     if not need_dW:
@@ -298,7 +300,7 @@ def muon_experts_grad(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, offset
     else:
         wt = _tensor(dW, "dW", device=dev)
         _shaped(dW, (e, o, d), "dW")
-    _call("muon_experts_grad", dev, dy.data_ptr(), x.data_ptr(), W.data_ptr(), offsets.data_ptr(), n, e, o, d,
+    _call("muon_experts_grad", dev, dy.data_ptr(), None if x is None else x.data_ptr(), W.data_ptr(), offsets.data_ptr(), n, e, o, d,
           None if dx is None else dx.data_ptr(), None if dW is None else dW.data_ptr(), wt, bool(accumulate),
           _error(error, dev))
     return dx, dW

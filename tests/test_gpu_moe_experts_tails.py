@@ -59,3 +59,11 @@ def test_added_right_behind_the_kernel_that_wrote_it():
         ns.muon_experts_grad(dy, x, W, offsets, dW=dW, need_dx=False)
         same.append((dW == alone).all())
     assert torch.stack(same).all()
+
+
+def test_the_rows_gradient_needs_no_rows():
+    x, W, dy, offsets = _inputs([33, 5, 0, 200], 264, 520, 6)
+    ref = ns.muon_experts_grad(dy, x, W, offsets, need_dW=False)[0]
+    assert torch.equal(ns.muon_experts_grad(dy, None, W, offsets, need_dW=False)[0], ref)
+    with pytest.raises(TypeError):
+        ns.muon_experts_grad(dy, None, W, offsets)
