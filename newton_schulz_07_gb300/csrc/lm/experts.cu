@@ -186,8 +186,9 @@ int muon_experts_grad(const muon_bf16* dy, const muon_bf16* x, const muon_bf16* 
   P.sectors = dim % 16 == 0 && aligned(dW, 32) ? 1 : 0;
   if (!map_bf16(&P.tmA, dy, out_dim, rows, 1, mns::kBlockK) || !map_bf16(&P.tmB[0], x, dim, rows, 1, mns::kBlockK))
     return MUON_NS_ERR_CUDA;
+  static constexpr int kTailRows[kExpTails] = {1, 2, 3, 4, 8, 12, 16, 32, 48};
   for (int i = 0; i < kExpTails; ++i)
-    if (!map_bf16(&P.tail[0][i], dy, out_dim, rows, 1, 1 << i) || !map_bf16(&P.tail[1][i], x, dim, rows, 1, 1 << i))
+    if (!map_bf16(&P.tail[0][i], dy, out_dim, rows, 1, kTailRows[i]) || !map_bf16(&P.tail[1][i], x, dim, rows, 1, kTailRows[i]))
       return MUON_NS_ERR_CUDA;
   const long long units = experts * tiles_of(out_dim) * tiles_of(dim);
   if (dW_type == MUON_LM_BF16) return status_of(launch_experts<kExpDwBf16>(P, units, stream));

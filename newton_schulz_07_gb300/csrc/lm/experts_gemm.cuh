@@ -17,9 +17,9 @@
 //
 // dW's contraction runs over the expert's rows, and its last 16 may hold rows of
 // others, which have to be zero in both operands.  The copies see to it: a stage that
-// ends so is brought in boxes of 32 rows to one that hold the expert's rows alone,
-// and the rest of the 16 in boxes that start behind the last row of x, where a copy
-// reads zeros.  (Nothing but copies writes the stages, so the copies' own barrier
+// ends so is brought in up to three boxes of 48 rows to one that hold the expert's
+// rows alone, and the rest of the 16 in a box that starts behind the last row of x,
+// where a copy reads zeros.  (Nothing but copies writes the stages, so the copies' own barrier
 // orders all of it for the MMA, in both CTAs.  Rows zeroed by a warp would have to
 // be handed from one CTA to the other with a release at cluster scope, about 2000
 // cycles.)
@@ -51,7 +51,7 @@ constexpr int kExpMax = 1024;      // experts
 constexpr int kExpBand = 16;       // row tiles of an expert that are walked together
 constexpr int kExpAhead = 16;      // units that a producer finds at once
 constexpr int kExpBoxes = 4;       // B boxes: of 128, 64, 32 or 16 rows
-constexpr int kExpTails = 6;       // dW's last rows: boxes of 1, 2, 4, 8, 16 or 32 of them
+constexpr int kExpTails = 9;       // dW's last rows: boxes of 1, 2, 3, 4, 8, 12, 16, 32 or 48 of them
 constexpr long long kExpDrain = 4000000000LL;
 constexpr uint32_t kExpNan = 0x7FFF7FFFu;  // NaN of fp32 and of bf16 alike
 
@@ -352,11 +352,14 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
   // bytes do.)
   auto box_of = [&](const Unit& t) { return kDw || t.half > 64 ? 0 : t.half > 32 ? 1 : t.half > 16 ? 2 : 3; };
   auto b_bytes_of = [&](const Unit& t) { return 16384u >> box_of(t); };
-  // Bytes of A in k-block kb of a unit, and of B.  (Of a stage that ends in others'
-  // rows those of its last 16 and before.)
+  // Rows of zeros behind the `left` of a stage that ends in others': 16 in one box,
+  // of which those past a multiple of 16 are not read, or as many as the stage has
+  // room for.
+  auto zeros_of = [](int left) { return left <= kBlockK - 16 ? 16 : kBlockK - left; };
+  // Bytes of A in k-block kb of a unit, and of B.
   auto a_bytes = [&](const Unit& t, int kb) {
     const int left = t.rows - kb * kK;
-    return kDw && others_rows(left) ? 256u * static_cast<uint32_t>((left + 15) & ~15) : static_cast<uint32_t>(kABytes);
+    return kDw && others_rows(left) ? 256u * static_cast<uint32_t>(left + zeros_of(left)) : static_cast<uint32_t>(kABytes);
   };
   auto b_bytes = [&](const Unit& t, int kb) { return kDw ? a_bytes(t, kb) : b_bytes_of(t); };
 
@@ -396,23 +399,27 @@ __global__ void __launch_bounds__(ExpSmem<MODE>::kThreads, 1) experts_gemm(const
             const int left = t.rows - kb * kK;
             tail = others_rows(left);
             if (tail) {
-              // Rows on from `row` of the stage, from row `from` of x or dy: the boxes of
-              // n rows' binary digits.  (A box may start at any row of the swizzle's
-              // pattern of 8, which goes by the shared-memory address.)
-              auto boxes = [&](int row, int n, int from, bool step) {
-#pragma unroll 1
-                for (int i = kExpTails - 1; i >= 0; --i) {
-                  if (!(n >> i & 1)) continue;
+              // To `row` on of the stage, from row `from` of x or dy on; zeros from behind
+              // the last.  (A box may start at any row of the swizzle's pattern of 8, which
+              // goes by the shared-memory address.)
+              auto box = [&](int row, int map, int from) {
 #pragma unroll
-                  for (int c = 0; c < 2; ++c)
-                    ptx::tma_load_3d_pair(to + c * EC::kMnChunkBytes + row * 128, &P.tail[loads_a ? 0 : 1][i], fb,
-                                          at + c * EC::kMnChunk, from, 0);
-                  row += 1 << i;
-                  if (step) from += 1 << i;
-                }
+                for (int c = 0; c < 2; ++c)
+                  ptx::tma_load_3d_pair(to + c * EC::kMnChunkBytes + row * 128, &P.tail[loads_a ? 0 : 1][map], fb,
+                                        at + c * EC::kMnChunk, from, 0);
               };
-              boxes(0, left, k0, true);
-              boxes(left, -left & 15, P.rows, false);  // behind the last row: zeros
+              auto few = [&](int row, int n, int from, bool zeros) {
+                const int n4 = n & 12, n1 = n & 3;
+                if (n4 != 0) box(row, 2 + n4 / 4, from);
+                if (n1 != 0) box(row + n4, n1 - 1, zeros ? from : from + n4);
+              };
+              const int n16 = left & 48, zeros = zeros_of(left);
+              if (n16 != 0) box(0, 5 + n16 / 16, k0);
+              few(n16, left & 15, k0 + n16, false);
+              if (zeros == 16)
+                box(left, 6, P.rows);
+              else
+                few(left, zeros, P.rows, true);
             }
           }
           if (tail) {
