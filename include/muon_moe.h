@@ -45,7 +45,8 @@ extern "C" {
  * w_type; rstd ([rows], r) and dweight: fp32.  Limits: rows <= 2^30,
  * 1 <= dim <= 2^20 (dim 0 with rows > 0 is an error: its mean does not exist).
  * Any dim and any pointer aligned to its element type; the widest accesses that
- * dim and the pointers allow are used.
+ * dim and the pointers allow are used.  The mean of squares has to be within fp32:
+ * where it is not, r is 0.
  * ------------------------------------------------------------------------- */
 
 /* residual may be NULL (s is then not written: it is x, which y may not be where the
@@ -108,7 +109,9 @@ int muon_route(const void* logits, int type, long long tokens, int experts, int 
                cudaStream_t stream);
 
 /* Gradient of sum(dgates gates): dlogits [tokens][experts] of type, which
- * overlaps nothing.  The choice itself has no gradient. */
+ * overlaps nothing.  The choice itself has no gradient.  chosen as muon_route
+ * writes it, an expert once a token.  Renormalised, the choices' logits alone are
+ * read: a NaN among the others is in the gates, not here. */
 int muon_route_grad(const float* dgates, const void* logits, int type, const int* chosen, long long tokens, int experts,
                     int k, int renormalize, void* dlogits, cudaStream_t stream);
 
@@ -146,7 +149,7 @@ int muon_combine_grad(const void* dout, const void* y, int type, const int* slot
  *   [0, rows] count as the nearest bound, and nothing outside the arrays is
  *   touched whatever they hold (where they decrease, some rows may get no value).
  * Limits: rows <= 2^30, experts <= 1024, out_dim, dim <= 2^20, fewer than 2^30
- * tiles of 256 x 256; out_dim and dim multiples of 8 (for muon_experts8 dim a
+ * tiles of 128 rows x 256 features (dW: of 256 x 256); out_dim and dim multiples of 8 (for muon_experts8 dim a
  * multiple of 16) and arrays 16-byte aligned: MUON_NS_ERR_ALIGNMENT otherwise.
  * Outputs (`device_error` among them) overlap nothing.  Products accumulate in fp32 on
  * the tensor cores.

@@ -56,9 +56,10 @@ cudaError_t launch_experts(const ExpertsParam<MODE>& P, long long units, cudaStr
   if (most == 0) {
     e = cudaFuncSetAttribute(experts_gemm<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    // TMEM loads write their registers some time after they are issued.  A build
-    // that spills registers around them is not run: one of the 8-bit form, with 128
-    // sums a thread, ended in a launch failure.
+    // A build that spills registers is not run.  TMEM loads write their registers some
+    // time after they are issued, and a build of the 8-bit form that spilled around
+    // them ended in a launch failure.  That the spilling was the cause is a suspicion:
+    // the same build also issued MMAs from a lane that had not polled their barrier.
     cudaFuncAttributes a;
     e = cudaFuncGetAttributes(&a, experts_gemm<MODE>);
     if (e != cudaSuccess) return e;
