@@ -45,8 +45,8 @@ extern "C" {
  * w_type; rstd ([rows], r) and dweight: fp32.  Limits: rows <= 2^30,
  * 1 <= dim <= 2^20 (dim 0 with rows > 0 is an error: its mean does not exist).
  * Any dim and any pointer aligned to its element type; the widest accesses that
- * dim and the pointers allow are used.  The mean of squares has to be within fp32:
- * where it is not, r is 0.
+ * dim and the pointers allow are used.  The mean of squares is an fp32 number: where
+ * it passes the largest r is 0, and squares below the smallest are lost.
  * ------------------------------------------------------------------------- */
 
 /* residual may be NULL (s is then not written: it is x, which y may not be where the

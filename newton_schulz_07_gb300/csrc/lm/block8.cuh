@@ -1,5 +1,7 @@
 // Rows in blocks of 128 columns, the blocks of 8-bit storage: how a group of
-// threads holds a row, and a block's way into e4m3 with a scale.
+// threads holds a row, and a block's way into e4m3 with a scale.  (Here and in the
+// other kernels of a block with experts no pointer is __restrict__: they start beside
+// the kernel before them, so what that one writes is not read-only while they run.)
 #pragma once
 
 #include "lm/common.cuh"

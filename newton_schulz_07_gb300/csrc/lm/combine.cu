@@ -32,7 +32,7 @@ __device__ __forceinline__ int slot_of(const Combine& C, long long i) {
 // are on their way at once (a token's k of up to 8: with 8 whatever the k, 4 of
 // 2048 columns held twice the registers and took 90 us for 55 at 16384 tokens).
 template <typename T, int VEC, int KB>
-__global__ void __launch_bounds__(256) combine_fwd(const Combine C, const T* __restrict__ y, T* __restrict__ out) {
+__global__ void __launch_bounds__(256) combine_fwd(const Combine C, const T* y, T* out) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int c = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
@@ -64,8 +64,8 @@ __global__ void __launch_bounds__(256) combine_fwd(const Combine C, const T* __r
 // SPLIT warps of a CTA share a token (few tokens), or each takes one.
 template <typename T, int VEC, int SPLIT, int KB>
 __global__ void __launch_bounds__(256)
-    combine_bwd(const Combine C, const T* __restrict__ dout, const T* __restrict__ y, T* __restrict__ dy,
-                float* __restrict__ dgates) {
+    combine_bwd(const Combine C, const T* dout, const T* y, T* dy,
+                float* dgates) {
   __shared__ float red[8][KB];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();

@@ -14,7 +14,7 @@ namespace {
 // are 64 bands.
 template <typename T, int W, int BAND>
 __global__ void __launch_bounds__(256)
-    quantize8(const T* __restrict__ x, long long rows, int dim, uint8_t* __restrict__ q, float* __restrict__ scales) {
+    quantize8(const T* x, long long rows, int dim, uint8_t* q, float* scales) {
   using B = Blk<W>;
   constexpr int kTake = 32 / B::kLanes;  // rows a warp takes at once
   constexpr int kRows = BAND > 1 ? BAND : 64;

@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(256) rms_norm_dw_long(const RmsGrad<T, TW> R) 
 // dweight from `parts` partial rows: a CTA takes 32 columns, its warps every 8th
 // partial, and the warps' sums are added in order.
 __global__ void __launch_bounds__(256)
-    rms_norm_join(const float* __restrict__ part, int parts, int dim, float* __restrict__ dweight) {
+    rms_norm_join(const float* part, int parts, int dim, float* dweight) {
   __shared__ float red[8][32];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();

@@ -61,7 +61,7 @@ __device__ __forceinline__ float warp_max(float v) {
 // The choice of one token, by a warp, of its logits z: lane j < k <= KM gets the
 // expert (or -1) and the gate of choice j.
 template <typename T, int J, int KM>
-__device__ __forceinline__ int choose(const T* __restrict__ z, int experts, int k, bool renormalize, float* gate) {
+__device__ __forceinline__ int choose(const T* z, int experts, int k, bool renormalize, float* gate) {
   const int lane = threadIdx.x & 31;
   float v[J];
   uint32_t o[J], e[J];
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(ONE ? 1024 : 512) route_choose(const Route R) 
 
 // Counts of the tiles before, in place, and of all: a CTA takes 32 experts, its
 // warps consecutive parts of the tiles.
-__global__ void __launch_bounds__(1024) route_scan(int* __restrict__ counts, int tiles, int experts, int* __restrict__ totals) {
+__global__ void __launch_bounds__(1024) route_scan(int* counts, int tiles, int experts, int* totals) {
   __shared__ int part[32][33];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -304,8 +304,8 @@ __global__ void __launch_bounds__(512) route_place(const Route R) {
 // experts, k 8: 23.3 us; with dg - inner, as first written, 19.9.)
 template <typename T, int J>
 __global__ void __launch_bounds__(256)
-    route_grad(const float* __restrict__ dgates, const T* __restrict__ logits, const int* __restrict__ chosen,
-               long long tokens, int experts, int k, T* __restrict__ dlogits) {
+    route_grad(const float* dgates, const T* logits, const int* chosen,
+               long long tokens, int experts, int k, T* dlogits) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31;
@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(256)
 // warp in accesses of V elements.
 template <typename T, int G, int V>
 __global__ void __launch_bounds__(256)
-    route_grad_chosen(const float* __restrict__ dgates, const T* __restrict__ logits, const int* __restrict__ chosen,
-                      long long tokens, int experts, int k, T* __restrict__ dlogits) {
+    route_grad_chosen(const float* dgates, const T* logits, const int* chosen,
+                      long long tokens, int experts, int k, T* dlogits) {
   constexpr int kTokens = 32 / G;  // of a warp
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
