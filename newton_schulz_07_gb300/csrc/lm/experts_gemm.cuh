@@ -17,12 +17,13 @@
 //
 // dW's contraction runs over the expert's rows, and its last 16 may hold rows of
 // others, which have to be zero in both operands.  The copies see to it: a stage that
-// ends so is brought in up to three boxes of 48 rows to one that hold the expert's
-// rows alone, and the rest of the 16 in a box that starts behind the last row of x,
-// where a copy reads zeros.  (Nothing but copies writes the stages, so the copies' own barrier
-// orders all of it for the MMA, in both CTAs.  Rows zeroed by a warp would have to
-// be handed from one CTA to the other with a release at cluster scope, about 2000
-// cycles.)
+// ends so is brought in up to three boxes that hold the expert's rows alone, and the
+// rest of the 16 in a box that starts behind the last row of x, where a copy reads
+// zeros.  Nothing but copies writes the stages, so the copies' own barrier orders all
+// of it for the MMA, in both CTAs.  (Rows zeroed by a warp would have to be handed
+// from one CTA to the other with a release at cluster scope, about 2000 cycles.  Boxes
+// of the rows' binary digits took 379 us for 369 at 65536 rows of 128 experts, 1536 x
+// 2048; without any ragged expert 344.)
 //
 // Roles: warp 0 loads A by TMA (each CTA its 128 rows) into a ring of 6 stages
 // (kExp8: 3 of two k-blocks) and warp 3 its half of B (one thread that loaded both
